@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,13 +20,16 @@ STATUS_NAMES = {0: "OK", 1: "NULLPTR", 2: "DTYPE", 3: "SHAPE", 4: "ATTR", 5: "UN
                 7: "WORKSPACE", 8: "HIP"}
 # element types (gmmfr_dtype)
 DT_NONE, DT_INT8, DT_INT4, DT_INT32, DT_INT64, DT_FLOAT32, DT_BFLOAT16 = range(7)
-DT_FLOAT8_E4M3FN, DT_FLOAT4_E2M1X2, DT_FLOAT8_E8M0 = 7, 8, 9
+DT_FLOAT8_E4M3FN, DT_FLOAT4_E2M1X2, DT_FLOAT8_E8M0, DT_FLOAT16 = 7, 8, 9, 10
 COMBINE = {"auto": 0, "atomic": 1, "ordered": 2}
 COMBINE_HYBRID = 3  # reported by the plan only
 
 EXPORTED = ("gmm_finalize_routing_workspace", "gmm_finalize_routing", "gmm_finalize_routing_profiled",
             "gmm_finalize_routing_plan", "gmmfr_status_string", "gmm_quant_permute_workspace",
-            "gmm_quant_permute", "gmm_quant_permute_profiled", "gmm_finalize_routing_noalloc")
+            "gmm_quant_permute", "gmm_quant_permute_profiled", "gmm_finalize_routing_noalloc",
+            "gmm_grouped_matmul_workspace", "gmm_grouped_matmul", "gmm_grouped_matmul_wgrad_workspace",
+            "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize")
+ACTIVATION = {None: 0, "none": 0, "swiglu": 1}
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GMMFR_NOALLOC_SCRATCH_BYTES
 
 
@@ -60,6 +64,27 @@ class QpArgs(ctypes.Structure):
         ("pertoken_scale", Tensor), ("logit", Tensor), ("row_index", Tensor), ("group_list", Tensor),
         ("expert_offset", ctypes.c_int64), ("group_list_type", ctypes.c_int64),
     ]
+
+
+class GmArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", Tensor), ("w", Tensor), ("x_scale", Tensor), ("w_scale", Tensor), ("group_list", Tensor), ("y", Tensor),
+        ("group_list_type", ctypes.c_int64), ("transpose_w", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
+    ]
+
+
+class GwArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", Tensor), ("dy", Tensor), ("group_list", Tensor), ("dw", Tensor),
+        ("group_list_type", ctypes.c_int64), ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
+    ]
+
+
+class MqArgs(ctypes.Structure):
+    _fields_ = [("x", Tensor), ("codes", Tensor), ("scales", Tensor), ("transpose", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -97,6 +122,15 @@ def lib():
         L.gmm_quant_permute_profiled.argtypes = [ctypes.POINTER(QpArgs), ctypes.c_void_p, ctypes.c_size_t,
                                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
         L.gmm_quant_permute_profiled.restype = ctypes.c_int
+        for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad"):
+            args = ctypes.POINTER(GwArgs if name.endswith("wgrad") else GmArgs)
+            getattr(L, name + "_workspace").argtypes = [args, ctypes.POINTER(ctypes.c_size_t)]
+            getattr(L, name + "_workspace").restype = ctypes.c_int
+            getattr(L, name).argtypes = [args, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("gmm_mx_quantize", "gmm_mx_dequantize"):
+            getattr(L, name).argtypes = [ctypes.POINTER(MqArgs), ctypes.c_void_p]
+            getattr(L, name).restype = ctypes.c_int
         L.gmmfr_status_string.argtypes = [ctypes.c_int]
         L.gmmfr_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -355,3 +389,202 @@ def _quant_permute_on(hidden, expert_ids, num_experts, topk_weights, expert_offs
     del keep
     out["workspace"] = workspace
     return out
+
+
+# ------------------------------------------------- grouped products and MX quantisation
+
+_pack_tensor = struct.Struct("=Qii4q").pack
+_ABSENT = _pack_tensor(0, 0, 0, 0, 0, 0, 0)
+_PAD = {n: (0,) * (4 - n) for n in range(5)}
+_codes_of: dict = {}
+
+
+def _packed(t) -> bytes:
+    """The bytes of a gmmfr_tensor (these calls are short: one struct, filled
+    at once, instead of a field at a time)."""
+    if t is None:
+        return _ABSENT
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    shape = t.shape
+    if len(shape) > 4:
+        raise ValueError("at most 4 dimensions")
+    code = _codes_of.get(t.dtype)
+    if code is None:
+        import torch
+        code = DT_FLOAT16 if t.dtype == torch.float16 else _dtype_code(t)
+        _codes_of[t.dtype] = code
+    return _pack_tensor(t.data_ptr(), code, len(shape), *shape, *_PAD[len(shape)])
+
+
+def _packed_tuning(tuning_config):
+    """(host array or None, the two fields' bytes)"""
+    if not tuning_config:
+        return None, bytes(16)
+    tuning = (ctypes.c_int64 * len(tuning_config))(*[int(v) for v in tuning_config])
+    return tuning, struct.pack("=Qq", ctypes.addressof(tuning), len(tuning_config))
+
+
+def make_gm_args(x, w, group_list, y, *, x_scale=None, w_scale=None, group_list_type: int = 0,
+                 transpose_w: bool = False, activation: Optional[str] = None,
+                 tuning_config: Optional[Sequence[int]] = None):
+    """C arguments of gmm_grouped_matmul.  Returns (args, keepalive), as make_args."""
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = b"".join((_packed(x), _packed(w), _packed(x_scale), _packed(w_scale), _packed(group_list), _packed(y),
+                    struct.pack("=qii", group_list_type, bool(transpose_w), ACTIVATION[activation]), tail))
+    return GmArgs.from_buffer_copy(raw), (x, w, group_list, y, x_scale, w_scale, tuning)
+
+
+def make_gw_args(x, dy, group_list, dw, *, group_list_type: int = 0, accumulate: bool = False,
+                 tuning_config: Optional[Sequence[int]] = None):
+    """C arguments of gmm_grouped_matmul_wgrad.  Returns (args, keepalive)."""
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = b"".join((_packed(x), _packed(dy), _packed(group_list), _packed(dw),
+                    struct.pack("=qii", group_list_type, bool(accumulate), 0), tail))
+    return GwArgs.from_buffer_copy(raw), (x, dy, group_list, dw, tuning)
+
+
+def make_mq_args(x, codes, scales, *, transpose: bool = False):
+    """C arguments of gmm_mx_quantize and gmm_mx_dequantize.  Returns (args, keepalive)."""
+    raw = b"".join((_packed(x), _packed(codes), _packed(scales), struct.pack("=ii", bool(transpose), 0)))
+    return MqArgs.from_buffer_copy(raw), (x, codes, scales)
+
+
+def _check_device(dev, *tensors) -> None:
+    """The kernels dereference these pointers on `dev`: all tensors live there."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must be on one device: {t.device} and {dev}")
+
+
+def _on(dev, stream, call):
+    """call(raw stream handle) with `dev` current and, where a stream is given,
+    that stream too (so that what the call allocates comes from its pool)."""
+    import torch
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return call(torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        ts = _torch_stream(stream)
+        if ts.device != dev:
+            raise ValueError(f"the stream is on {ts.device}, the tensors on {dev}")
+        with torch.cuda.stream(ts):
+            return call(ts.cuda_stream)
+
+
+def _two_stage(name: str, args, workspace, dev, handle) -> None:
+    """Size the workspace, allocate it if none is given, enqueue."""
+    import torch
+    L = lib()
+    need = ctypes.c_size_t(0)
+    st = getattr(L, name + "_workspace")(args, need)
+    if st != OK:
+        raise GmmfrError(st, name + "_workspace")
+    if workspace is None and need.value:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    ptr, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = getattr(L, name)(args, ptr, size, handle)
+    if st != OK:
+        raise GmmfrError(st, name)
+
+
+def grouped_matmul(x, w, group_list, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
+                   group_list_type: int = 0, transpose_w: bool = False, activation: Optional[str] = None,
+                   tuning_config: Optional[Sequence[int]] = None, workspace=None, stream=None):
+    """Rows of x, sorted by expert and split by group_list, times their
+    expert's weights; activation "swiglu": silu of the product's first n/2
+    columns times the others.  16-bit x and w (weights (e,k,n), or (e,n,k) with
+    transpose_w: then this is also the gradient towards the rows of a product
+    with (e,k,n) weights), or microscaled x (FP8 or FP4) and FP4 w (e,n,k) with
+    their scales.  Returns out, allocated as (m, n or n/2) if none is given, in
+    out_dtype (default: x's type; bf16 for microscaled x); rows behind the last
+    group are left as they are."""
+    import torch
+    dev = x.device
+    _check_device(dev, w, group_list, x_scale, w_scale, out, workspace)
+
+    def call(handle):
+        y = out
+        if y is None:
+            columns = w.shape[1 if transpose_w else 2] // (2 if ACTIVATION[activation] else 1)
+            dtype = out_dtype or (x.dtype if x.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16)
+            y = torch.empty((x.shape[0], columns), dtype=dtype, device=dev)
+        args, keep = make_gm_args(x, w, group_list, y, x_scale=x_scale, w_scale=w_scale,
+                                  group_list_type=group_list_type, transpose_w=transpose_w, activation=activation,
+                                  tuning_config=tuning_config)
+        _two_stage("gmm_grouped_matmul", args, workspace, dev, handle)
+        del keep
+        return y
+    return _on(dev, stream, call)
+
+
+def grouped_matmul_wgrad(x, dy, group_list, *, out=None, out_dtype=None, accumulate: bool = False,
+                         group_list_type: int = 0, tuning_config: Optional[Sequence[int]] = None, workspace=None,
+                         stream=None):
+    """Gradient of a grouped product's weights (e,k,n): x_g^T dy_g for every
+    expert, in out_dtype (default fp32), zeros for one without rows.
+    accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x)."""
+    import torch
+    dev = x.device
+    _check_device(dev, dy, group_list, out, workspace)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+
+    def call(handle):
+        dw = out
+        if dw is None:
+            dw = torch.empty((group_list.shape[0], x.shape[1], dy.shape[1]), dtype=out_dtype or torch.float32, device=dev)
+        args, keep = make_gw_args(x, dy, group_list, dw, group_list_type=group_list_type, accumulate=accumulate,
+                                  tuning_config=tuning_config)
+        _two_stage("gmm_grouped_matmul_wgrad", args, workspace, dev, handle)
+        del keep
+        return dw
+    return _on(dev, stream, call)
+
+
+def mx_quantize(x, *, format: str = "fp4", transpose: bool = False, stream=None):
+    """(codes, scales) of x (rows,k) or (e,n,k), or with transpose of weights
+    (e,k,n), which become (e,n,k): FP4 (k/2 bytes a row) or FP8 codes with one
+    E8M0 scale per 32 values, (..., k/64, 2)."""
+    import torch
+    dev = x.device
+    _check_device(dev)
+    if format not in ("fp4", "fp8"):
+        raise ValueError(f"unknown format {format!r}")
+    if transpose and x.dim() != 3:
+        raise ValueError("transpose takes weights (e,k,n)")
+
+    def call(handle):
+        lead, k = ((x.shape[0], x.shape[2]), x.shape[1]) if transpose else (tuple(x.shape[:-1]), x.shape[-1])
+        if format == "fp4":
+            codes = torch.empty((*lead, k // 2), dtype=torch.float4_e2m1fn_x2, device=dev)
+        else:
+            codes = torch.empty((*lead, k), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((*lead, k // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
+        args, keep = make_mq_args(x, codes, scales, transpose=transpose)
+        st = lib().gmm_mx_quantize(args, handle)
+        if st != OK:
+            raise GmmfrError(st, "gmm_mx_quantize")
+        del keep
+        return codes, scales
+    return _on(dev, stream, call)
+
+
+def mx_dequantize(codes, scales, *, dtype=None, stream=None):
+    """The values that codes and scales stand for, (rows,k) or (e,n,k), in
+    dtype (bf16 by default, fp16 or fp32)."""
+    import torch
+    dev = codes.device
+    _check_device(dev, scales)
+
+    def call(handle):
+        per = 2 if codes.dtype == torch.float4_e2m1fn_x2 else 1
+        x = torch.empty((*codes.shape[:-1], codes.shape[-1] * per), dtype=dtype or torch.bfloat16, device=dev)
+        args, keep = make_mq_args(x, codes, scales)
+        st = lib().gmm_mx_dequantize(args, handle)
+        if st != OK:
+            raise GmmfrError(st, "gmm_mx_dequantize")
+        del keep
+        return x
+    return _on(dev, stream, call)

@@ -2,21 +2,24 @@
 
     python -m quantized_moe_grouped_amd.build
 """
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmmfr.so")
 SOURCES = [os.path.join(CSRC, "gmmfr_kernels.hip"), os.path.join(CSRC, "gmmfr_api.cpp"),
-           os.path.join(CSRC, "quant_permute.hip")]
+           os.path.join(CSRC, "quant_permute.hip"), os.path.join(CSRC, "grouped_matmul.hip"),
+           os.path.join(CSRC, "mx_quant.hip")]
 ARCH = os.environ.get("GMMFR_ARCH", "gfx950")
 
 FLAGS = [
-    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
+    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
     "-ffp-contract=off",
     # packed fp32 VALU forms stay disabled
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -32,12 +35,7 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS]
-    for src in SOURCES:
-        cmd += ["-x", "hip", src]
-    cmd += ["-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -48,6 +46,17 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def build(verbose: bool = False) -> str:
+    """One object per source, compiled side by side, and one link."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as objdir:
+        objs = [os.path.join(objdir, os.path.basename(src) + ".o") for src in SOURCES]
+        cmds = [[hipcc(), *FLAGS, "-c", "-x", "hip", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
+        with concurrent.futures.ThreadPoolExecutor(max_workers=len(cmds)) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,981 @@
+// Products grouped by expert, without a combine: rows of x sorted by expert
+// and split by groupList, each group multiplied by its expert's weights, and
+// the gradient of the weights.
+//
+//   product:  y[i][j]     = sum_q x[i][q] * w[g(i)][q][j]
+//   SwiGLU:   y[i][j]     = u / (1 + exp(-u)) * v,  u = column j and v = column n/2 + j of the product
+//   wgrad:    dw[g][p][j] = sum_{i in g} x[i][p] * dy[i][j]
+//
+// Operands are bf16 or fp16, or microscaled: FP8 E4M3 or FP4 E2M1 rows with
+// FP4 E2M1 weights and one E8M0 scale per 32 values along the reduction.
+// Sums run in fp32 on the matrix cores; the result is rounded once, on
+// storing.
+//
+// One kernel template, product_kernel: C(M,N) += A(M,R) * B(R,N) over the
+// tiles of all experts.  In the product M is the group's rows, N the weight
+// columns and R = k; in wgrad M = k, N = n and R the group's rows, which both
+// operands then hold along their slow axis.
+//
+//   - The grid is persistent; tiles come in a raster that gives each XCD
+//     blocks of neighbouring tiles (shared operand panels in its L2).
+//   - Operands go HBM -> LDS with buffer_load_dwordx4 ... lds, 16 bytes per
+//     lane, no VGPRs.  The buffer descriptor ends with the group's last row
+//     (or the reduction's last row), so whatever lies past it arrives in LDS
+//     as zeros: ragged groups and odd sizes need no other masking and no row
+//     of another group is multiplied.
+//   - The copies of one running stream of k-steps cross tile borders: the
+//     next tile's first stages load under the present tile's epilogue.
+//   - v_mfma_f32_32x32x16_{bf16,f16} or v_mfma_scale_f32_32x32x64_f8f6f4 with
+//     the weights as the instruction's A operand and the rows as B: each lane
+//     then holds four neighbouring columns of one row, and a swap of two
+//     registers between the wave's halves makes them eight, stored in 16
+//     bytes.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+#include <type_traits>
+
+#include "../../include/gmmfr.h"
+
+namespace gmmgm {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+#define LDS_PTR(T) __attribute__((address_space(3))) T*
+
+constexpr int kMaxExperts = 1024;
+constexpr int kXcds = 8;
+constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every descriptor's end
+
+// operand encodings
+enum Enc { kBf16 = 0, kF16 = 1, kFp4 = 2, kFp8 = 3 };  // of the rows; weights: the same, or FP4 with kFp4 and kFp8
+enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2 };
+
+struct Params {
+  const void* x;             // (m,k); 16-bit, FP8, or FP4 (m,k/2)
+  const void* w;             // weights, or dy (m,n) for wgrad
+  const uint8_t* xs;         // E8M0 (m, k/32)
+  const uint8_t* ws;         // E8M0 (e, n, k/32)
+  const int64_t* group_list; // (e)
+  void* y;                   // (m, n or n/2), or dw (e,k,n)
+  int64_t m, k, n;
+  int32_t e, cumulative;     // groupList holds ends (type 0) instead of counts
+  int32_t tiles_m, tiles_n;  // tiles along M (wgrad) and N
+  int32_t out, accumulate;
+};
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(const LDS_PTR(void))p; }
+
+// 16 (or 4) bytes per lane from buffer `r` at byte offset `off` to LDS: lane i
+// of the wave fills [lds + 16 i, lds + 16 i + 16).  Offsets at or past the
+// descriptor's end give zeros.  Inline asm because the compiler would
+// otherwise wait for every copy in flight before each LDS read; the kernel
+// waits itself (wait_vmcnt) before the barrier that publishes a stage.  No
+// output registers; M0 is used by nothing else here.
+__device__ __forceinline__ void copy16(v4i r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(v4i r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+               : "memory");
+}
+
+// A raw buffer over [base, base + bytes), bytes clamped to [0, 2^31].
+__device__ __forceinline__ v4i buffer(const void* base, int64_t bytes) {
+  const int64_t b = uniform64((int64_t)base);
+  const int64_t n = bytes < 0 ? 0 : (bytes > (int64_t)kOutside ? (int64_t)kOutside : bytes);
+  return v4i{(int)b, (int)((b >> 32) & 0xFFFF), __builtin_amdgcn_readfirstlane((int)n), 0x00020000};
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// Barrier that publishes this wave's LDS writes and finished reads, without
+// waiting for copies in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// LDS position of 16-byte chunk c of row r, C chunks a row.  Rows along the
+// reduction's fast axis: 16 rows read at one chunk index (ds_read_b128) fall
+// on 16 different chunks of the 256-byte bank window.
+template <int C>
+__device__ __forceinline__ int swz_row(int r) {
+  if constexpr (C == 4) return ((r >> 1) ^ (r >> 3)) & 3;
+  else if constexpr (C == 8) return (r ^ ((r >> 3) & 1)) & 7;
+  else return r & 15;
+}
+// Rows across the reduction, read with ds_read_b64_tr_b16: one read of 32
+// lanes touches 4 rows x 4 chunks (lanes 0-31) or 2 x 4 rows x 2 chunks; the
+// rows' chunks are moved apart by whole groups of 4 chunks, and by 2 for the
+// second set of rows.  Two rows of 8 chunks share one window: only bit 1 of r
+// needs the move there.
+template <int C>
+__device__ __forceinline__ int swz_col(int r) {
+  if constexpr (C >= 16) return ((r & 3) << 2) | (((r >> 3) & 1) << 1);
+  else return (((r >> 1) & 1) << 2) | (((r >> 3) & 1) << 1);
+}
+
+// groupList -> s_ends[g] (end row of expert g) and s_pre[g] (tiles before
+// expert g; s_pre[e] = all).  Device data are not trusted: entries are clamped
+// to [0, m], type-0 ends become the running maximum and type-1 ends the
+// running sum capped at m.  Every wave scans 64 entries a round in registers
+// (all loads first); one wave writes.  Sums of two values below 2^31 fit 32
+// bits, so the capped sum needs no more.
+__device__ void group_table(const Params& p, int bm, int32_t* s_ends, int32_t* s_pre) {
+  const int lane = threadIdx.x & 63;
+  constexpr int kRounds = kMaxExperts / 64;
+  const int rounds = (p.e + 63) / 64;
+  uint32_t v[kRounds];
+#pragma unroll
+  for (int b = 0; b < kRounds; ++b) {
+    v[b] = 0;
+    if (b < rounds) {
+      const int g = b * 64 + lane;
+      const int64_t c = g < p.e ? p.group_list[g] : 0;
+      v[b] = (uint32_t)(c < 0 ? 0 : (c > p.m ? p.m : c));
+    }
+  }
+  const uint32_t m = (uint32_t)p.m;
+  uint32_t end_carry = 0, tile_carry = 0;
+  const bool writer = threadIdx.x < 64;
+#pragma unroll
+  for (int b = 0; b < kRounds; ++b) {
+    if (b < rounds) {
+      const int g = b * 64 + lane;
+      uint32_t x = v[b];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)x, d);
+        if (lane >= d) x = p.cumulative ? max(x, o) : min(x + o, m);
+      }
+      x = p.cumulative ? max(x, end_carry) : min(x + end_carry, m);
+      uint32_t before = (uint32_t)__shfl_up((int)x, 1);
+      if (lane == 0) before = end_carry;
+      end_carry = (uint32_t)__shfl((int)x, 63);
+      uint32_t t = g < p.e ? ((x - before + bm - 1) / bm) * (uint32_t)p.tiles_n : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)t, d);
+        if (lane >= d) t += o;
+      }
+      t += tile_carry;
+      tile_carry = (uint32_t)__shfl((int)t, 63);
+      if (writer && g < p.e) {
+        s_ends[g] = (int32_t)x;
+        s_pre[g + 1] = (int32_t)t;
+      }
+    }
+  }
+  if (threadIdx.x == 0) s_pre[0] = 0;
+  __syncthreads();
+}
+
+struct Tile {
+  int g;          // expert
+  int64_t m0;     // first row along M: a row of x, or of dw
+  int valid;      // rows of the tile that exist
+  int64_t n0;     // first column (SwiGLU: of y)
+  int64_t r0, r1; // the reduction's range (wgrad: the group's rows)
+};
+
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+// ENC: operand encoding.  XCOL / WCOL: the operand's fast axis is M / N (16
+// bit only) instead of the reduction.  WGRAD: see above.  GLU: SwiGLU
+// epilogue; the tile's columns alternate 32 gate columns and the 32 up columns
+// that belong to them.  KWAVES: all waves compute the whole tile, each on its
+// own slice of every stage, and their sums meet in LDS (few rows: the weights
+// are streamed once and the tile is narrow).
+template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int BM, int BN, int BK, int WM, int WN, int STAGES,
+          bool KWAVES, int OCC>
+__global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
+  constexpr int NWAVES = WM * WN, NT = NWAVES * 64;
+  constexpr bool MX = ENC == kFp4 || ENC == kFp8;
+  static_assert(!MX || (!XCOL && !WCOL && !WGRAD), "microscaled operands run along the reduction");
+  constexpr int XBITS = ENC == kFp4 ? 4 : (ENC == kFp8 ? 8 : 16), WBITS = MX ? 4 : 16;
+  constexpr int KSLICE = MX ? 64 : 16;  // reduction length of one matrix instruction
+  constexpr int NS = BK / KSLICE;       // slices of a stage
+  constexpr int MY_M = KWAVES ? 1 : WM, MY_N = KWAVES ? 1 : WN;  // waves across the tile
+  constexpr int WTM = BM / MY_M, WTN = BN / MY_N, FM = WTM / 32, FN = WTN / 32;
+  static_assert(FM >= 1 && FN >= 1 && FM * 32 * MY_M == BM && FN * 32 * MY_N == BN && (!GLU || FN % 2 == 0), "tile");
+  static_assert(!KWAVES || NS == NWAVES, "one slice of a stage for each wave");
+  // chunks of a stage row: BK values along the reduction, or BM / BN across it
+  constexpr int XC = XCOL ? BM / 8 : BK * XBITS / 128, WC = WCOL ? BN / 8 : BK * WBITS / 128;
+  constexpr int X_BYTES = BM * BK * XBITS / 8, W_BYTES = BN * BK * WBITS / 8;
+  constexpr int XI = X_BYTES / 16 / NT, WI = W_BYTES / 16 / NT;  // copies of a thread for one stage
+  static_assert(XI >= 1 && WI >= 1 && XI * 16 * NT == X_BYTES && WI * 16 * NT == W_BYTES, "whole copies");
+  static_assert((XCOL || NT / XC % 16 == 0) && (WCOL || NT / WC % 16 == 0), "one swizzle for all copies of a lane");
+  constexpr int STEP_COPIES = XI + WI;
+  static_assert((STAGES - 2) * STEP_COPIES < 64, "vmcnt range");
+  // E8M0 scales: 16 bytes a row at a time, the scales of 512 values
+  constexpr int SPG = MX ? 512 / BK : 1;  // k-steps of one group of scales
+  constexpr int XW = (BM + 63) / 64, SROWS = MX ? XW * 64 + BN : 1;  // rows whose scales are staged
+  static_assert(!MX || XW + BN / 64 <= NWAVES, "a thread for each row's scales");
+
+  __shared__ __attribute__((aligned(16))) uint8_t sX[STAGES * X_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sW[STAGES * W_BYTES];
+  // groups of scales: up to STAGES - 1 in flight (a tile may end within a
+  // group) and the one in use
+  __shared__ __attribute__((aligned(16))) v4u s_sc[MX ? STAGES * SROWS : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t s_sc2[MX ? STAGES * SROWS : 1];
+  __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? (NWAVES - 1) * FM * FN * 4 * 64 : 1];
+  extern __shared__ __attribute__((aligned(16))) int32_t s_dyn[];
+  int32_t* s_ends = s_dyn;
+  int32_t* s_pre = s_dyn + p.e;
+
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = KWAVES ? 0 : wave / WN, wn = KWAVES ? 0 : wave % WN;
+  group_table(p, WGRAD ? 1 : BM, s_ends, s_pre);
+  const int total = WGRAD ? p.e * p.tiles_m * p.tiles_n : s_pre[p.e];
+  const int64_t F = GLU ? p.n / 2 : p.n;  // columns of y
+  const int64_t x_row = WGRAD ? p.k * 2 : p.k * XBITS / 8;  // bytes
+  const int64_t w_row = WCOL ? p.n * 2 : p.k * WBITS / 8;
+  const int64_t s_row = p.k / 32;
+
+  // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
+  // (workgroup b runs on XCD b % 8), at most 64 a block and fewer when there
+  // are few tiles, so that every XCD gets some
+  const int G = gridDim.x;
+  const int block = min(64, (total + kXcds - 1) / kXcds);
+  auto tile_at = [&](int j) -> int {
+    int64_t t;
+    if (G % kXcds == 0) {
+      const int i = j * (G / kXcds) + (int)blockIdx.x / kXcds;
+      t = ((int64_t)(i / block) * kXcds + blockIdx.x % kXcds) * block + i % block;
+    } else {
+      t = (int64_t)j * G + blockIdx.x;
+    }
+    return t < total ? (int)t : -1;
+  };
+  auto coord = [&](int t) -> Tile {
+    Tile c;
+    int local, mtiles;
+    if constexpr (WGRAD) {
+      c.g = t / (p.tiles_m * p.tiles_n);
+      local = t - c.g * p.tiles_m * p.tiles_n;
+      mtiles = p.tiles_m;
+    } else {
+      int lo = 0, hi = p.e - 1;  // the largest g with s_pre[g] <= t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pre[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      c.g = __builtin_amdgcn_readfirstlane(lo);
+      local = t - s_pre[c.g];
+      mtiles = 0;
+    }
+    const int64_t begin = c.g ? s_ends[c.g - 1] : 0, end = s_ends[c.g];
+    if constexpr (!WGRAD) mtiles = (int)((end - begin + BM - 1) / BM);
+    // inside an expert: groups of GM tiles along M, N swept inside a group
+    constexpr int GM = BM >= 256 ? 4 : 8;
+    const int grp = local / (GM * p.tiles_n), in = local - grp * GM * p.tiles_n;
+    const int size = min(GM, mtiles - grp * GM);
+    const int mt = grp * GM + in % size, nt = in / size;
+    c.m0 = uniform64((WGRAD ? 0 : begin) + (int64_t)mt * BM);
+    c.valid = __builtin_amdgcn_readfirstlane((int)min((int64_t)BM, (WGRAD ? p.k : end) - c.m0));
+    c.n0 = uniform64((int64_t)nt * (GLU ? BN / 2 : BN));
+    c.r0 = uniform64(WGRAD ? begin : 0);
+    c.r1 = uniform64(WGRAD ? end : p.k);
+    return c;
+  };
+  auto steps_of = [&](const Tile& c) -> int {
+    const int s = (int)((c.r1 - c.r0 + BK - 1) / BK);
+    return WGRAD ? max(s, 1) : s;  // an expert without rows: one step of zeros
+  };
+
+  // column of the weights for column q of the tile; -1 past the last
+  auto column = [&](const Tile& c, int q) -> int64_t {
+    if constexpr (GLU) {
+      const int64_t f = c.n0 + (q >> 6) * 32 + (q & 31);
+      return f < F ? f + ((q & 32) ? F : 0) : -1;
+    } else {
+      return c.n0 + q < p.n ? c.n0 + q : -1;
+    }
+  };
+
+  // ---- the copy stream's state: sources of the tile it is in
+  const uint8_t* x_base = nullptr;
+  const uint8_t* w_base = nullptr;
+  const uint8_t* xs_base = nullptr;
+  const uint8_t* ws_base = nullptr;
+  int64_t x_left = 0, w_left = 0;  // bytes from the base to the operand's end
+  uint32_t x_off[XI], w_off[WI], s_off = kOutside;
+  // whether this row's scales begin in the middle of a dword: in the stream's
+  // tile, and (a bit a slot) where the staged groups of scales came from
+  uint32_t s_odd = 0, odd_slots = 0;
+  const int x_ch = XCOL ? 0 : (lane % XC) ^ swz_row<XC>(tid / XC);
+  const int w_ch = WCOL ? 0 : (lane % WC) ^ swz_row<WC>(tid / WC);
+  const bool x_scales = wave < XW;  // waves that stage the rows' and the columns' scales
+  auto set_sources = [&](const Tile& c) {
+    if constexpr (XCOL) {  // wgrad: base at (first row, first column of the tile)
+      x_base = (const uint8_t*)p.x + (c.r0 * p.k + c.m0) * 2;
+      x_left = (c.r1 - c.r0) * x_row - c.m0 * 2;
+#pragma unroll
+      for (int q = 0; q < XI; ++q) {
+        const int slot = (q * NWAVES + wave) * 64 + lane, r = slot / XC;
+        const int col = ((slot % XC) ^ swz_col<XC>(r)) * 8;
+        x_off[q] = col < c.valid ? (uint32_t)(r * x_row + col * 2) : kOutside;
+      }
+    } else {
+      x_base = (const uint8_t*)p.x + c.m0 * x_row;
+      x_left = c.valid * x_row;
+#pragma unroll
+      for (int q = 0; q < XI; ++q) x_off[q] = (uint32_t)((q * (NT / XC) + tid / XC) * x_row + x_ch * 16);
+    }
+    if constexpr (WCOL) {  // base at the tile's first column, of the expert's first row (or the group's)
+      w_base = (const uint8_t*)p.w + ((WGRAD ? c.r0 : c.g * p.k) * p.n + c.n0) * 2;
+      w_left = (c.r1 - c.r0) * w_row - c.n0 * 2;
+#pragma unroll
+      for (int q = 0; q < WI; ++q) {
+        const int slot = (q * NWAVES + wave) * 64 + lane, r = slot / WC;
+        const int64_t col = column(c, ((slot % WC) ^ swz_col<WC>(r)) * 8);
+        w_off[q] = col >= 0 ? (uint32_t)(r * w_row + (col - c.n0) * 2) : kOutside;
+      }
+    } else {
+      w_base = (const uint8_t*)p.w + ((int64_t)c.g * p.n + c.n0) * w_row;
+      w_left = (p.n - c.n0) * w_row;
+#pragma unroll
+      for (int q = 0; q < WI; ++q) {
+        const int64_t col = column(c, q * (NT / WC) + tid / WC);
+        w_off[q] = col >= 0 ? (uint32_t)((col - c.n0) * w_row + w_ch * 16) : kOutside;
+      }
+    }
+    if constexpr (MX) {
+      // scales of row `tid` (the first XW waves) or column tid - XW * 64; a
+      // row's scales begin at a whole dword, or (k % 128 == 64, odd rows) two
+      // bytes after one, and are then read from that dword on
+      xs_base = p.xs + c.m0 * s_row;
+      ws_base = p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
+      int64_t off = -1;
+      const uint8_t* base = x_scales ? xs_base : ws_base;
+      if (x_scales) {
+        if (tid < c.valid) off = tid * s_row;
+      } else if (tid - XW * 64 < BN) {
+        const int64_t col = column(c, tid - XW * 64);
+        if (col >= 0) off = (col - c.n0) * s_row;
+      }
+      const int fine = (int)(((uintptr_t)base + off) & 3);
+      s_odd = fine != 0 ? 1u : 0u;
+      // relative to the base rounded down to a dword
+      s_off = off >= 0 ? (uint32_t)(off - fine + ((uintptr_t)base & 3)) : kOutside;
+    }
+  };
+  // copies of k-step kt of the stream's tile into stage `st`; slot: for its
+  // scales when the step begins a group of them
+  auto issue = [&](bool live, int kt, int st, int slot) {
+    if constexpr (MX) {
+      if (kt % SPG == 0) {
+        const bool mine = x_scales || wave < XW + BN / 64;
+        if (mine) {
+          const uint8_t* base = x_scales ? xs_base : ws_base;
+          const uint8_t* end = x_scales ? p.xs + p.m * s_row : p.ws + (int64_t)p.e * p.n * s_row;
+          const uint8_t* from = (const uint8_t*)((uintptr_t)base & ~(uintptr_t)3) + (kt / SPG) * 16;
+          // up to the end of the dword that holds the last scale (a dword
+          // that the descriptor cuts reads as zero)
+          const v4i r = buffer(from, live ? ((end - from) + 3) & ~(int64_t)3 : 0);
+          copy16(r, s_off, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc[slot * SROWS + wave * 64])));
+          if (s_row & 3) {
+            copy4(r, s_off + 16, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc2[slot * SROWS + wave * 64])));
+            odd_slots = (odd_slots & ~(1u << slot)) | s_odd << slot;
+          }
+        }
+      }
+    }
+    const int64_t xa = XCOL ? (int64_t)kt * BK * x_row : (int64_t)kt * (BK * XBITS / 8);
+    const int64_t wa = WCOL ? (int64_t)kt * BK * w_row : (int64_t)kt * (BK * WBITS / 8);
+    const v4i xr = buffer(x_base + xa, live ? x_left - xa : 0), wr = buffer(w_base + wa, live ? w_left - wa : 0);
+    // the last step of a reduction that is no multiple of BK: chunks past the
+    // row's end would be the next row's
+    const int64_t xe = XCOL ? 0 : x_row - xa, we = WCOL ? 0 : w_row - wa;
+    const bool x_in = XCOL || x_ch * 16 < xe, w_in = WCOL || w_ch * 16 < we;
+#pragma unroll
+    for (int q = 0; q < XI; ++q)
+      copy16(xr, x_in ? x_off[q] : kOutside,
+             __builtin_amdgcn_readfirstlane(lds_addr(sX + st * X_BYTES + (q * NWAVES + wave) * 1024)));
+#pragma unroll
+    for (int q = 0; q < WI; ++q)
+      copy16(wr, w_in ? w_off[q] : kOutside,
+             __builtin_amdgcn_readfirstlane(lds_addr(sW + st * W_BYTES + (q * NWAVES + wave) * 1024)));
+  };
+
+  // ---- fragments of slice s of stage st.  A fragment holds 32 rows (x) or
+  // columns (w): lane l row l % 32, and its h = l / 32 half of the slice.
+  using Frag = std::conditional_t<MX, v8i, v8s>;
+  auto frag_rows = [&](const uint8_t* st, int row, int s, auto c_, auto bits_) -> Frag {
+    constexpr int C = decltype(c_)::value, BITS = decltype(bits_)::value;
+    const int z = swz_row<C>(row);
+    const uint8_t* a = st + row * (C * 16);
+    if constexpr (!MX) {
+      return *(const LDS_PTR(v8s))(a + (((2 * s + h) ^ z) << 4));
+    } else if constexpr (BITS == 4) {
+      const v4i v = *(const LDS_PTR(v4i))(a + (((2 * s + h) ^ z) << 4));
+      return v8i{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+    } else {
+      const v4i lo = *(const LDS_PTR(v4i))(a + (((4 * s + h) ^ z) << 4));
+      const v4i hi = *(const LDS_PTR(v4i))(a + (((4 * s + 2 + h) ^ z) << 4));
+      return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    }
+  };
+  // transposing read: within 16 lanes, lane i receives element i % 16 of the
+  // four rows addressed by lanes 4 b .. 4 b + 3 (b = 0..3, 4 elements each)
+  auto frag_cols = [&](const uint8_t* st, int first, int s, auto c_) -> v8s {
+    constexpr int C = decltype(c_)::value;
+    const int i = lane & 15, grp = lane >> 4;
+    const int r = s * 16 + (grp >> 1) * 8 + (i >> 2), col = first + (grp & 1) * 16 + (i & 3) * 4;
+    const uint8_t* a = st + r * (C * 16) + ((((col >> 3) ^ swz_col<C>(r)) << 4) | ((col & 7) << 1));
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(v4s))a);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(v4s))(a + 4 * C * 16));
+    return v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  };
+  auto read_frags = [&](int st, int s, Frag (&xf)[FM], Frag (&wf)[FN]) {
+    const uint8_t* xb = sX + st * X_BYTES;
+    const uint8_t* wb = sW + st * W_BYTES;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (XCOL) xf[i] = frag_cols(xb, wm * WTM + i * 32, s, std::integral_constant<int, XC>{});
+      else xf[i] = frag_rows(xb, wm * WTM + i * 32 + (lane & 31), s, std::integral_constant<int, XC>{},
+                             std::integral_constant<int, XBITS>{});
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (WCOL) wf[j] = frag_cols(wb, wn * WTN + j * 32, s, std::integral_constant<int, WC>{});
+      else wf[j] = frag_rows(wb, wn * WTN + j * 32 + (lane & 31), s, std::integral_constant<int, WC>{},
+                             std::integral_constant<int, WBITS>{});
+    }
+  };
+  // this step's scale bytes, one register a fragment: byte b is slice b's
+  uint32_t xsc[FM], wsc[FN];
+  auto read_scales = [&](int kt, int slot) {
+    if constexpr (MX) {
+      const int q0 = (kt % SPG) * NS;  // first slice of the step among the group's eight
+      const int shift = KWAVES ? 8 * ((q0 + wave) & 3) : 8 * (q0 & 3), word = (KWAVES ? q0 + wave : q0) >> 2;
+      const uint32_t* base = (const uint32_t*)&s_sc[slot * SROWS] + h * 2 + word;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xsc[i] = base[(wm * WTM + i * 32 + (lane & 31)) * 4] >> shift;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) wsc[j] = base[(XW * 64 + wn * WTN + j * 32 + (lane & 31)) * 4] >> shift;
+    }
+  };
+  // a landed group of scales, in place and by the thread that copied it: bytes of even
+  // blocks (the lanes with h = 0) and odd ones set apart; blocks past k become
+  // zero bytes (2^-127, never the NaN a neighbouring row may hold)
+  auto sort_scales = [&](int kt, int slot) {
+    if constexpr (MX) {
+      if (x_scales || wave < XW + BN / 64) {
+        v4u v = s_sc[slot * SROWS + wave * 64 + lane];
+        if (s_row & 3) {
+          const uint32_t next = s_sc2[slot * SROWS + wave * 64 + lane];
+          if ((odd_slots >> slot) & 1u)
+            v = v4u{__builtin_amdgcn_alignbyte(v.y, v.x, 2), __builtin_amdgcn_alignbyte(v.z, v.y, 2),
+                    __builtin_amdgcn_alignbyte(v.w, v.z, 2), __builtin_amdgcn_alignbyte(next, v.w, 2)};
+        }
+        const int pairs = (int)min((int64_t)8, (s_row - (int64_t)(kt / SPG) * 16) / 2);
+        const uint64_t keep = pairs >= 8 ? ~0ull : (1ull << (8 * pairs)) - 1;
+        const uint32_t k0 = (uint32_t)keep, k1 = (uint32_t)(keep >> 32);
+        s_sc[slot * SROWS + wave * 64 + lane] =
+            v4u{__builtin_amdgcn_perm(v.y, v.x, 0x06040200u) & k0, __builtin_amdgcn_perm(v.w, v.z, 0x06040200u) & k1,
+                __builtin_amdgcn_perm(v.y, v.x, 0x07050301u) & k0, __builtin_amdgcn_perm(v.w, v.z, 0x07050301u) & k1};
+      }
+    }
+  };
+
+  v16f acc[FM][FN];
+  auto multiply = [&](Frag (&xf)[FM], Frag (&wf)[FN], auto s_) {
+    constexpr int S = decltype(s_)::value & 3;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (ENC == kBf16)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, wf[j]),
+                                                              __builtin_bit_cast(v8bf, xf[i]), acc[i][j], 0, 0, 0);
+        else if constexpr (ENC == kF16)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, wf[j]),
+                                                             __builtin_bit_cast(v8h, xf[i]), acc[i][j], 0, 0, 0);
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf[i], acc[i][j], 4, ENC == kFp4 ? 4 : 0, S,
+                                                                      (int)wsc[j], S, (int)xsc[i]);
+      }
+  };
+
+  // ---- epilogue: lane l holds row l % 32 of each 32 x 32 block and columns
+  // 8 (r / 4) + 4 h + r % 4, r = 0..15
+  const int64_t y_row = F;
+  auto store_block = [&](const Tile& c, int i, int col, const float (&v)[16]) {
+    const int row = wm * WTM + i * 32 + (lane & 31);
+    if (row >= c.valid) return;
+    const int64_t at = (WGRAD ? (int64_t)c.g * p.k * p.n : 0) + (c.m0 + row) * y_row;
+    if (p.out == kOutF32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = c.n0 + col + 8 * q + 4 * h;
+        if (n >= F) continue;
+        v4f o = v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        v4f* d = (v4f*)((float*)p.y + at + n);
+        if (WGRAD && p.accumulate) {
+          const v4f old = *d;
+          o = v4f{o.x + old.x, o.y + old.y, o.z + old.z, o.w + old.w};
+        }
+        *d = o;
+      }
+    } else {
+      uint32_t d[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (p.out == kOutBf16) {
+          typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+          d[q] = __builtin_bit_cast(uint32_t, v2bf{(__bf16)v[2 * q], (__bf16)v[2 * q + 1]});
+        } else {
+          typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+          d[q] = __builtin_bit_cast(uint32_t, v2h{(_Float16)v[2 * q], (_Float16)v[2 * q + 1]});
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        // columns 16 q .. 16 q + 15: after the swap the lower half holds the
+        // first eight, the upper half the others.  Both halves hold the same
+        // row, so both are here.
+        const auto a = __builtin_amdgcn_permlane32_swap(d[4 * q], d[4 * q + 2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(d[4 * q + 1], d[4 * q + 3], false, false);
+        const int64_t n = c.n0 + col + 16 * q + 8 * h;
+        if (n < F) *(v4u*)((uint16_t*)p.y + at + n) = v4u{a[0], b[0], a[1], b[1]};
+      }
+    }
+  };
+  auto epilogue = [&](const Tile& c) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (GLU) {
+#pragma unroll
+        for (int j = 0; j < FN; j += 2) {
+          float v[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float u = acc[i][j][r];
+            v[r] = u / (1.0f + expf(-u)) * acc[i][j + 1][r];
+          }
+          store_block(c, i, (wn * WTN + j * 32) / 2, v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          float v[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+          store_block(c, i, wn * WTN + j * 32, v);
+        }
+      }
+    }
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = v16f{0};
+  };
+
+  // ---- the two streams
+  const int t0 = tile_at(0);
+  if (t0 < 0) return;
+  int jl = 0, lk = 0, sc_in = 0;  // copies: tile count, k-step in it, slot of the next scales
+  bool live = true;
+  Tile lc = coord(t0);
+  int lsteps = steps_of(lc);
+  set_sources(lc);
+  auto feed = [&](int st) {
+    issue(live, lk, st, sc_in);
+    if constexpr (MX) {
+      if (lk % SPG == 0) sc_in = sc_in + 1 == STAGES ? 0 : sc_in + 1;
+    }
+    if (++lk == lsteps) {
+      lk = 0;
+      if (live) {
+        const int t = tile_at(++jl);
+        if (t >= 0) {
+          lc = coord(t);
+          lsteps = steps_of(lc);
+          set_sources(lc);
+        } else {
+          live = false;  // what is still issued copies zeros
+        }
+      }
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) feed(s);
+  int st = 0, slot = STAGES - 1;  // computing: stage, slot of the scales in use
+  int kt = 0, jc = 0;
+  Tile c = coord(t0);
+  int steps = steps_of(c);
+  // the step `nk` of the computing stream has landed (its copies and all
+  // before them): sort its scales if it begins a group of them, and publish
+  auto publish = [&](int nk) {
+    wait_vmcnt<(STAGES - 2) * STEP_COPIES>();
+    if constexpr (MX) {
+      if (nk % SPG == 0) {
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        sort_scales(nk, slot);
+      }
+    }
+    lds_barrier();
+  };
+  if constexpr (KWAVES) {
+    while (true) {
+      clear();
+#pragma unroll 1
+      for (kt = 0; kt < steps; ++kt) {
+        publish(kt);
+        feed(st == 0 ? STAGES - 1 : st - 1);
+        Frag xf[FM], wf[FN];
+        read_scales(kt, slot);
+        read_frags(st, wave, xf, wf);
+        multiply(xf, wf, std::integral_constant<int, 0>{});
+        st = st + 1 == STAGES ? 0 : st + 1;
+      }
+      // the waves' sums meet in the first wave (its own first, then ascending)
+      if (wave > 0) {
+#pragma unroll
+        for (int q = 0; q < FM * FN * 4; ++q) {
+          const v16f& a = acc[q / 4 / FN][q / 4 % FN];
+          s_sum[((wave - 1) * FM * FN * 4 + q) * 64 + lane] =
+              v4f{a[q % 4 * 4], a[q % 4 * 4 + 1], a[q % 4 * 4 + 2], a[q % 4 * 4 + 3]};
+        }
+      }
+      lds_barrier();
+      if (wave == 0) {
+#pragma unroll
+        for (int w = 0; w < NWAVES - 1; ++w)
+#pragma unroll
+          for (int q = 0; q < FM * FN * 4; ++q) {
+            const v4f o = s_sum[(w * FM * FN * 4 + q) * 64 + lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + r] += o[r];
+          }
+        epilogue(c);
+      }
+      const int t = tile_at(++jc);
+      if (t < 0) break;
+      c = coord(t);
+      steps = steps_of(c);
+      // s_sum is written again only after the next tile's first barrier
+    }
+  } else {
+    static_assert(KWAVES || NS % 2 == 0, "fragment buffers alternate");
+    Frag xf[2][FM], wf[2][FN];
+    publish(0);
+    read_scales(0, slot);
+    read_frags(0, 0, xf[0], wf[0]);
+    while (true) {
+      clear();
+      int t_next = -1;
+#pragma unroll 1
+      for (kt = 0; kt < steps; ++kt) {
+        // every wave has read the stage before this one: refill it
+        feed(st == 0 ? STAGES - 1 : st - 1);
+        static_for<NS - 1>([&](auto s_) {
+          constexpr int S = decltype(s_)::value;
+          read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+          multiply(xf[S & 1], wf[S & 1], s_);
+        });
+        st = st + 1 == STAGES ? 0 : st + 1;
+        const bool last = kt + 1 == steps;
+        if (last) t_next = tile_at(++jc);
+        if (!last || t_next >= 0) {
+          // the next step's first fragments are read before this step's last
+          // products; its scales after them
+          publish(last ? 0 : kt + 1);
+          read_frags(st, 0, xf[0], wf[0]);
+        }
+        multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{});
+        if (!last || t_next >= 0) read_scales(last ? 0 : kt + 1, slot);
+      }
+      epilogue(c);
+      if (t_next < 0) break;
+      c = coord(t_next);
+      steps = steps_of(c);
+    }
+  }
+  wait_vmcnt<0>();  // no copy in flight when the workgroup ends
+}
+
+
+// ---------------------------------------------------------------- host side
+
+bool given(const gmmfr_tensor& t) {
+  if (t.data != nullptr) return true;
+  for (int i = 0; i < t.ndim && i < 4; ++i)
+    if (t.dims[i] == 0) return true;
+  return false;
+}
+bool shape_is(const gmmfr_tensor& t, int nd, int64_t d0, int64_t d1 = 0, int64_t d2 = 0, int64_t d3 = 0) {
+  const int64_t d[4] = {d0, d1, d2, d3};
+  if (t.ndim != nd) return false;
+  for (int i = 0; i < nd; ++i)
+    if (t.dims[i] != d[i]) return false;
+  return true;
+}
+int aligned(std::initializer_list<const gmmfr_tensor*> all) {
+  for (const gmmfr_tensor* t : all)
+    if (given(*t) && ((uintptr_t)t->data & 15u) != 0) return GMMFR_ERR_ALIGN;
+  return GMMFR_OK;
+}
+
+enum Kind { kLarge = 0, kMiddle = 1, kSmall = 2 };
+constexpr int kTileM[3] = {256, 128, 32}, kTileN[3] = {256, 128, 64}, kPerCu[3] = {1, 2, 2};
+
+struct Plan {
+  Params p;
+  Kind kind;
+  int enc, grid;
+  bool glu, col;
+};
+
+// tuning: [0] expected rows per expert, [1] forced tile height, [2] cap of the grid
+int tuning(const int64_t* t, int64_t len, int64_t* rows, int64_t* height, int64_t* cap) {
+  *rows = *height = *cap = 0;
+  if (len < 0 || (len > 0 && !t)) return GMMFR_ERR_ATTR;
+  if (len > 0) *rows = t[0];
+  if (len > 1) *height = t[1];
+  if (len > 2) *cap = t[2];
+  if (*rows < 0 || *cap < 0) return GMMFR_ERR_ATTR;
+  if (*height != 0 && *height != 32 && *height != 128 && *height != 256) return GMMFR_ERR_ATTR;
+  return GMMFR_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int grid_of(const Plan& pl, int64_t tiles, int64_t cap) {
+  int64_t g = 256 * kPerCu[pl.kind];
+  if (cap > 0 && cap < g) g = cap;
+  // fewer workgroups than that only in whole rounds of the XCDs
+  if (tiles < g) g = cap > 0 && cap < kXcds ? tiles : ceil_div(tiles, kXcds) * kXcds;
+  if (cap > 0 && cap < g) g = cap;
+  return (int)(g < 1 ? 1 : g);
+}
+
+int product_plan(const gmmgm_args* a, Plan* pl) {
+  if (!a) return GMMFR_ERR_NULLPTR;
+  if (!given(a->x) || !given(a->w) || !given(a->group_list) || !given(a->y)) return GMMFR_ERR_NULLPTR;
+  const int xt = a->x.dtype, wt = a->w.dtype, yt = a->y.dtype;
+  const bool mx = xt == GMMFR_DT_FLOAT4_E2M1X2 || xt == GMMFR_DT_FLOAT8_E4M3FN;
+  if (mx) {
+    if (wt != GMMFR_DT_FLOAT4_E2M1X2) return GMMFR_ERR_DTYPE;
+    if (!given(a->x_scale) || !given(a->w_scale)) return GMMFR_ERR_NULLPTR;
+    if (a->x_scale.dtype != GMMFR_DT_FLOAT8_E8M0 || a->w_scale.dtype != GMMFR_DT_FLOAT8_E8M0) return GMMFR_ERR_DTYPE;
+    if (yt != GMMFR_DT_BFLOAT16 && yt != GMMFR_DT_FLOAT16 && yt != GMMFR_DT_FLOAT32) return GMMFR_ERR_DTYPE;
+  } else {
+    if (xt != GMMFR_DT_BFLOAT16 && xt != GMMFR_DT_FLOAT16) return GMMFR_ERR_DTYPE;
+    if (wt != xt || (yt != xt && yt != GMMFR_DT_FLOAT32)) return GMMFR_ERR_DTYPE;
+    if (given(a->x_scale) || given(a->w_scale)) return GMMFR_ERR_UNSUPPORTED;
+  }
+  if (a->group_list.dtype != GMMFR_DT_INT64) return GMMFR_ERR_DTYPE;
+  if (a->group_list_type != 0 && a->group_list_type != 1) return GMMFR_ERR_ATTR;
+  if (a->transpose_w != 0 && a->transpose_w != 1) return GMMFR_ERR_ATTR;
+  if (mx && a->transpose_w != 1) return GMMFR_ERR_ATTR;
+  if (a->activation != GMMGM_ACT_NONE && a->activation != GMMGM_ACT_SWIGLU) return GMMFR_ERR_ATTR;
+  int64_t rows, height, cap;
+  if (tuning(a->tuning_config, a->tuning_config_len, &rows, &height, &cap) != GMMFR_OK) return GMMFR_ERR_ATTR;
+  const bool glu = a->activation == GMMGM_ACT_SWIGLU;
+  if (a->x.ndim != 2 || a->w.ndim != 3 || a->group_list.ndim != 1) return GMMFR_ERR_SHAPE;
+  const int per = xt == GMMFR_DT_FLOAT4_E2M1X2 ? 2 : 1, wper = mx ? 2 : 1;  // values an element of the shape stands for
+  const int64_t m = a->x.dims[0], k = a->x.dims[1] * per, e = a->w.dims[0];
+  const int64_t n = a->w.dims[a->transpose_w ? 1 : 2], wk = a->w.dims[a->transpose_w ? 2 : 1] * wper;
+  if (m < 0 || m >= (int64_t(1) << 31) || e < 1 || e > kMaxExperts) return GMMFR_ERR_SHAPE;
+  const int64_t unit = mx ? 64 : 8;
+  if (k < unit || k > 65536 || k % unit != 0 || wk != k) return GMMFR_ERR_SHAPE;
+  const int64_t nunit = glu ? 16 : 8;
+  if (n < nunit || n > 65536 || n % nunit != 0 || m * n >= (int64_t(1) << 40)) return GMMFR_ERR_SHAPE;
+  // SwiGLU reaches n/2 weight columns away from a tile's own: 31-bit offsets
+  if (glu && a->transpose_w && n * k * (mx ? 1 : 4) / 2 > (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
+  if (a->group_list.dims[0] != e) return GMMFR_ERR_SHAPE;
+  if (mx && (!shape_is(a->x_scale, 3, m, k / 64, 2) || !shape_is(a->w_scale, 4, e, n, k / 64, 2))) return GMMFR_ERR_SHAPE;
+  if (!shape_is(a->y, 2, m, glu ? n / 2 : n)) return GMMFR_ERR_SHAPE;
+  if (aligned({&a->x, &a->w, &a->x_scale, &a->w_scale, &a->group_list, &a->y}) != GMMFR_OK) return GMMFR_ERR_ALIGN;
+  Params& p = pl->p;
+  p.x = a->x.data;
+  p.w = a->w.data;
+  p.xs = (const uint8_t*)a->x_scale.data;
+  p.ws = (const uint8_t*)a->w_scale.data;
+  p.group_list = (const int64_t*)a->group_list.data;
+  p.y = a->y.data;
+  p.m = m;
+  p.k = k;
+  p.n = n;
+  p.e = (int32_t)e;
+  p.cumulative = a->group_list_type == 0;
+  p.out = yt == GMMFR_DT_FLOAT32 ? kOutF32 : (yt == GMMFR_DT_FLOAT16 ? kOutF16 : kOutBf16);
+  p.accumulate = 0;
+  pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : xt == GMMFR_DT_FLOAT16 ? kF16 : per == 2 ? kFp4 : kFp8;
+  pl->glu = glu;
+  pl->col = a->transpose_w == 0;
+  // rows an expert is likely to have: experts without rows cost nothing
+  const int64_t avg = rows > 0 ? rows : m / (e < m ? e : (m > 0 ? m : 1));
+  pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
+                    : (avg >= 192 ? kLarge : avg > 32 ? kMiddle : kSmall);
+  const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
+  p.tiles_m = 0;
+  p.tiles_n = (int32_t)ceil_div(glu ? n / 2 : n, tn);
+  // at most this many tiles: whole ones, and one part a non-empty expert
+  const int64_t tiles = (m / kTileM[pl->kind] + (e < m ? e : m)) * p.tiles_n;
+  if (tiles >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
+  pl->grid = grid_of(*pl, tiles, cap);
+  return GMMFR_OK;
+}
+
+int wgrad_plan(const gmmgw_args* a, Plan* pl) {
+  if (!a) return GMMFR_ERR_NULLPTR;
+  if (!given(a->x) || !given(a->dy) || !given(a->group_list) || !given(a->dw)) return GMMFR_ERR_NULLPTR;
+  const int xt = a->x.dtype, ot = a->dw.dtype;
+  if (xt != GMMFR_DT_BFLOAT16 && xt != GMMFR_DT_FLOAT16) return GMMFR_ERR_DTYPE;
+  if (a->dy.dtype != xt || (ot != xt && ot != GMMFR_DT_FLOAT32)) return GMMFR_ERR_DTYPE;
+  if (a->group_list.dtype != GMMFR_DT_INT64) return GMMFR_ERR_DTYPE;
+  if (a->group_list_type != 0 && a->group_list_type != 1) return GMMFR_ERR_ATTR;
+  if (a->accumulate != 0 && (a->accumulate != 1 || ot != GMMFR_DT_FLOAT32)) return GMMFR_ERR_ATTR;
+  int64_t rows, height, cap;
+  if (tuning(a->tuning_config, a->tuning_config_len, &rows, &height, &cap) != GMMFR_OK || height == 32)
+    return GMMFR_ERR_ATTR;
+  if (a->x.ndim != 2 || a->dy.ndim != 2 || a->group_list.ndim != 1) return GMMFR_ERR_SHAPE;
+  const int64_t m = a->x.dims[0], k = a->x.dims[1], n = a->dy.dims[1], e = a->group_list.dims[0];
+  if (m < 0 || m >= (int64_t(1) << 31) || a->dy.dims[0] != m || e < 1 || e > kMaxExperts) return GMMFR_ERR_SHAPE;
+  if (k < 8 || k > 65536 || k % 8 != 0 || n < 8 || n > 65536 || n % 8 != 0) return GMMFR_ERR_SHAPE;
+  if (!shape_is(a->dw, 3, e, k, n)) return GMMFR_ERR_SHAPE;
+  if (aligned({&a->x, &a->dy, &a->group_list, &a->dw}) != GMMFR_OK) return GMMFR_ERR_ALIGN;
+  Params& p = pl->p;
+  p.x = a->x.data;
+  p.w = a->dy.data;
+  p.xs = p.ws = nullptr;
+  p.group_list = (const int64_t*)a->group_list.data;
+  p.y = a->dw.data;
+  p.m = m;
+  p.k = k;
+  p.n = n;
+  p.e = (int32_t)e;
+  p.cumulative = a->group_list_type == 0;
+  p.out = ot == GMMFR_DT_FLOAT32 ? kOutF32 : (ot == GMMFR_DT_FLOAT16 ? kOutF16 : kOutBf16);
+  p.accumulate = a->accumulate;
+  pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : kF16;
+  pl->glu = false;
+  pl->col = true;
+  const int64_t large = e * ceil_div(k, 256) * ceil_div(n, 256);
+  pl->kind = height ? (height == 256 ? kLarge : kMiddle) : (large >= 512 ? kLarge : kMiddle);
+  p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);
+  p.tiles_n = (int32_t)ceil_div(n, kTileN[pl->kind]);
+  pl->grid = grid_of(*pl, e * p.tiles_m * p.tiles_n, cap);
+  return GMMFR_OK;
+}
+
+template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU>
+void launch(const Plan& pl, hipStream_t s) {
+  const size_t dyn = (size_t)(2 * pl.p.e + 1) * 4;
+  constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
+  if (pl.kind == kLarge)
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, BK, 4, 2, 2, false, 2>), dim3(pl.grid),
+                       dim3(512), dyn, s, pl.p);
+  else if (pl.kind == kMiddle)
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>), dim3(pl.grid),
+                       dim3(256), dyn, s, pl.p);
+  else if constexpr (!WGRAD)
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, 4, true, 2>), dim3(pl.grid),
+                       dim3(256), dyn, s, pl.p);
+}
+
+int product_run(const gmmgm_args* a, void* stream) {
+  Plan pl;
+  const int st = product_plan(a, &pl);
+  if (st != GMMFR_OK) return st;
+  if (pl.p.m == 0) return GMMFR_OK;
+  hipStream_t s = (hipStream_t)stream;
+  auto with = [&](auto enc_) {
+    constexpr int ENC = decltype(enc_)::value;
+    constexpr bool MX = ENC == kFp4 || ENC == kFp8;
+    if constexpr (!MX) {
+      if (pl.col) {
+        if (pl.glu) launch<ENC, false, true, false, true>(pl, s);
+        else launch<ENC, false, true, false, false>(pl, s);
+        return;
+      }
+    }
+    if (pl.glu) launch<ENC, false, false, false, true>(pl, s);
+    else launch<ENC, false, false, false, false>(pl, s);
+  };
+  if (pl.enc == kBf16) with(std::integral_constant<int, kBf16>{});
+  else if (pl.enc == kF16) with(std::integral_constant<int, kF16>{});
+  else if (pl.enc == kFp4) with(std::integral_constant<int, kFp4>{});
+  else with(std::integral_constant<int, kFp8>{});
+  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+}
+
+int wgrad_run(const gmmgw_args* a, void* stream) {
+  Plan pl;
+  const int st = wgrad_plan(a, &pl);
+  if (st != GMMFR_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (pl.enc == kBf16) launch<kBf16, true, true, true, false>(pl, s);
+  else launch<kF16, true, true, true, false>(pl, s);
+  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+}
+
+}  // namespace gmmgm
+
+extern "C" {
+
+using namespace gmmgm;
+
+int gmm_grouped_matmul_workspace(const gmmgm_args* args, size_t* workspace_bytes) {
+  Plan pl;
+  const int st = product_plan(args, &pl);
+  if (st != GMMFR_OK) return st;
+  if (!workspace_bytes) return GMMFR_ERR_NULLPTR;
+  *workspace_bytes = 0;
+  return GMMFR_OK;
+}
+
+int gmm_grouped_matmul(const gmmgm_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return product_run(args, stream);
+}
+
+int gmm_grouped_matmul_wgrad_workspace(const gmmgw_args* args, size_t* workspace_bytes) {
+  Plan pl;
+  const int st = wgrad_plan(args, &pl);
+  if (st != GMMFR_OK) return st;
+  if (!workspace_bytes) return GMMFR_ERR_NULLPTR;
+  *workspace_bytes = 0;
+  return GMMFR_OK;
+}
+
+int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return wgrad_run(args, stream);
+}
+
+}  // extern "C"
