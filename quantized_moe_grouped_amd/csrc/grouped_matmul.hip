@@ -190,11 +190,11 @@ __device__ void group_table(const Params& p, int bm, int32_t* s_ends, int32_t* s
 }
 
 struct Tile {
-  int g;          // expert
-  int64_t m0;     // first row along M: a row of x, or of dw
-  int valid;      // rows of the tile that exist
-  int64_t n0;     // first column (SwiGLU: of y)
-  int64_t r0, r1; // the reduction's range (wgrad: the group's rows)
+  int g;       // expert
+  int m0;      // first row along M: a row of x, or of dw
+  int valid;   // rows of the tile that exist
+  int n0;      // first column (SwiGLU: of y)
+  int r0, r1;  // the reduction's range (wgrad: the group's rows)
 };
 
 template <int N, int I = 0, typename F>
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int MY_M = KWAVES ? 1 : WM, MY_N = KWAVES ? 1 : WN;  // waves across the tile
   constexpr int WTM = BM / MY_M, WTN = BN / MY_N, FM = WTM / 32, FN = WTN / 32;
   static_assert(FM >= 1 && FN >= 1 && FM * 32 * MY_M == BM && FN * 32 * MY_N == BN && (!GLU || FN % 2 == 0), "tile");
-  static_assert(!KWAVES || NS == NWAVES, "one slice of a stage for each wave");
+  static_assert(KWAVES ? NS == NWAVES : NS == 2 || NS == 4, "one slice of a stage for each wave, or two or four");
   // chunks of a stage row: BK values along the reduction, or BM / BN across it
   constexpr int XC = XCOL ? BM / 8 : BK * XBITS / 128, WC = WCOL ? BN / 8 : BK * WBITS / 128;
   constexpr int X_BYTES = BM * BK * XBITS / 8, W_BYTES = BN * BK * WBITS / 8;
@@ -239,11 +239,13 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
 
   __shared__ __attribute__((aligned(16))) uint8_t sX[STAGES * X_BYTES];
   __shared__ __attribute__((aligned(16))) uint8_t sW[STAGES * W_BYTES];
-  // groups of scales: up to STAGES - 1 in flight (a tile may end within a
-  // group) and the one in use
+  // groups of scales as they lie in memory, from the dword that holds a row's
+  // first one: up to STAGES - 1 in flight (a tile may end within a group) and
+  // the one in use.  s_sc2: the dword after the 16 bytes, for rows that begin
+  // in the middle of a dword.
   __shared__ __attribute__((aligned(16))) v4u s_sc[MX ? STAGES * SROWS : 1];
   __shared__ __attribute__((aligned(16))) uint32_t s_sc2[MX ? STAGES * SROWS : 1];
-  __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? (NWAVES - 1) * FM * FN * 4 * 64 : 1];
+  __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? 2 * FM * FN * 4 * 64 : 1];
   extern __shared__ __attribute__((aligned(16))) int32_t s_dyn[];
   int32_t* s_ends = s_dyn;
   int32_t* s_pre = s_dyn + p.e;
@@ -257,6 +259,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const int64_t x_row = WGRAD ? p.k * 2 : p.k * XBITS / 8;  // bytes
   const int64_t w_row = WCOL ? p.n * 2 : p.k * WBITS / 8;
   const int64_t s_row = p.k / 32;
+  const bool s_split = MX && (s_row & 3) != 0;  // k % 128 == 64: odd rows' scales begin mid-dword
 
   // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
   // (workgroup b runs on XCD b % 8), at most 64 a block and fewer when there
@@ -288,227 +291,260 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         else hi = mid - 1;
       }
       c.g = __builtin_amdgcn_readfirstlane(lo);
-      local = t - s_pre[c.g];
+      local = __builtin_amdgcn_readfirstlane(t - s_pre[c.g]);
       mtiles = 0;
     }
-    const int64_t begin = c.g ? s_ends[c.g - 1] : 0, end = s_ends[c.g];
-    if constexpr (!WGRAD) mtiles = (int)((end - begin + BM - 1) / BM);
+    const int begin = __builtin_amdgcn_readfirstlane(c.g ? s_ends[c.g - 1] : 0);
+    const int end = __builtin_amdgcn_readfirstlane(s_ends[c.g]);
+    if constexpr (!WGRAD) mtiles = (int)(((int64_t)end - begin + BM - 1) / BM);
     // inside an expert: groups of GM tiles along M, N swept inside a group
     constexpr int GM = BM >= 256 ? 4 : 8;
     const int grp = local / (GM * p.tiles_n), in = local - grp * GM * p.tiles_n;
     const int size = min(GM, mtiles - grp * GM);
     const int mt = grp * GM + in % size, nt = in / size;
-    c.m0 = uniform64((WGRAD ? 0 : begin) + (int64_t)mt * BM);
-    c.valid = __builtin_amdgcn_readfirstlane((int)min((int64_t)BM, (WGRAD ? p.k : end) - c.m0));
-    c.n0 = uniform64((int64_t)nt * (GLU ? BN / 2 : BN));
-    c.r0 = uniform64(WGRAD ? begin : 0);
-    c.r1 = uniform64(WGRAD ? end : p.k);
+    c.m0 = (WGRAD ? 0 : begin) + mt * BM;
+    c.valid = min(BM, (WGRAD ? (int)p.k : end) - c.m0);
+    c.n0 = nt * (GLU ? BN / 2 : BN);
+    c.r0 = WGRAD ? begin : 0;
+    c.r1 = WGRAD ? end : (int)p.k;
     return c;
   };
   auto steps_of = [&](const Tile& c) -> int {
-    const int s = (int)((c.r1 - c.r0 + BK - 1) / BK);
+    const int s = (int)(((int64_t)c.r1 - c.r0 + BK - 1) / BK);
     return WGRAD ? max(s, 1) : s;  // an expert without rows: one step of zeros
   };
 
   // column of the weights for column q of the tile; -1 past the last
-  auto column = [&](const Tile& c, int q) -> int64_t {
+  auto column = [&](const Tile& c, int q) -> int {
     if constexpr (GLU) {
-      const int64_t f = c.n0 + (q >> 6) * 32 + (q & 31);
-      return f < F ? f + ((q & 32) ? F : 0) : -1;
+      const int f = c.n0 + (q >> 6) * 32 + (q & 31);
+      return f < F ? f + ((q & 32) ? (int)F : 0) : -1;
     } else {
       return c.n0 + q < p.n ? c.n0 + q : -1;
     }
   };
 
-  // ---- the copy stream's state: sources of the tile it is in
-  const uint8_t* x_base = nullptr;
-  const uint8_t* w_base = nullptr;
-  const uint8_t* xs_base = nullptr;
-  const uint8_t* ws_base = nullptr;
-  int64_t x_left = 0, w_left = 0;  // bytes from the base to the operand's end
+  // ---- the copy stream's state: where the next step of its tile comes from
+  const uint8_t* x_at = nullptr;
+  const uint8_t* w_at = nullptr;
+  const uint8_t* s_at = nullptr;   // the row (first XW waves) or column scales, from a whole dword on
+  int64_t x_left = 0, w_left = 0, s_left = 0;  // bytes from there to the operand's end
+  int x_tail = 0, w_tail = 0;      // bytes from there to the end of a row along the reduction
   uint32_t x_off[XI], w_off[WI], s_off = kOutside;
-  // whether this row's scales begin in the middle of a dword: in the stream's
-  // tile, and (a bit a slot) where the staged groups of scales came from
-  uint32_t s_odd = 0, odd_slots = 0;
-  const int x_ch = XCOL ? 0 : (lane % XC) ^ swz_row<XC>(tid / XC);
-  const int w_ch = WCOL ? 0 : (lane % WC) ^ swz_row<WC>(tid / WC);
-  const bool x_scales = wave < XW;  // waves that stage the rows' and the columns' scales
+  const int x_ch = XCOL ? 0 : ((lane % XC) ^ swz_row<XC>(tid / XC)) * 16;
+  const int w_ch = WCOL ? 0 : ((lane % WC) ^ swz_row<WC>(tid / WC)) * 16;
+  const bool x_scales = wave < XW, any_scales = MX && wave < XW + BN / 64;
   auto set_sources = [&](const Tile& c) {
-    if constexpr (XCOL) {  // wgrad: base at (first row, first column of the tile)
-      x_base = (const uint8_t*)p.x + (c.r0 * p.k + c.m0) * 2;
+    // indices pass through an opaque point: the offsets are computed here,
+    // once a tile, and not kept in parts across the k-loop
+    int lane = threadIdx.x & 63, tid = threadIdx.x;
+    asm volatile("" : "+v"(lane), "+v"(tid));
+    if constexpr (XCOL) {  // wgrad: from (first row of the group, first column of the tile)
+      x_at = (const uint8_t*)p.x + ((int64_t)c.r0 * p.k + c.m0) * 2;
       x_left = (c.r1 - c.r0) * x_row - c.m0 * 2;
 #pragma unroll
       for (int q = 0; q < XI; ++q) {
-        const int slot = (q * NWAVES + wave) * 64 + lane, r = slot / XC;
+        const int slot = q * NT + tid, r = slot / XC;
         const int col = ((slot % XC) ^ swz_col<XC>(r)) * 8;
-        x_off[q] = col < c.valid ? (uint32_t)(r * x_row + col * 2) : kOutside;
+        x_off[q] = col < c.valid ? (uint32_t)(r * (int)x_row + col * 2) : kOutside;
       }
     } else {
-      x_base = (const uint8_t*)p.x + c.m0 * x_row;
+      x_at = (const uint8_t*)p.x + c.m0 * x_row;
       x_left = c.valid * x_row;
+      x_tail = (int)x_row;
 #pragma unroll
-      for (int q = 0; q < XI; ++q) x_off[q] = (uint32_t)((q * (NT / XC) + tid / XC) * x_row + x_ch * 16);
+      for (int q = 0; q < XI; ++q) x_off[q] = (uint32_t)((q * (NT / XC) + tid / XC) * (int)x_row + x_ch);
     }
-    if constexpr (WCOL) {  // base at the tile's first column, of the expert's first row (or the group's)
-      w_base = (const uint8_t*)p.w + ((WGRAD ? c.r0 : c.g * p.k) * p.n + c.n0) * 2;
+    if constexpr (WCOL) {  // from the tile's first column, of the expert's first row (or the group's)
+      w_at = (const uint8_t*)p.w + ((WGRAD ? (int64_t)c.r0 : c.g * p.k) * p.n + c.n0) * 2;
       w_left = (c.r1 - c.r0) * w_row - c.n0 * 2;
 #pragma unroll
       for (int q = 0; q < WI; ++q) {
-        const int slot = (q * NWAVES + wave) * 64 + lane, r = slot / WC;
-        const int64_t col = column(c, ((slot % WC) ^ swz_col<WC>(r)) * 8);
-        w_off[q] = col >= 0 ? (uint32_t)(r * w_row + (col - c.n0) * 2) : kOutside;
+        const int slot = q * NT + tid, r = slot / WC;
+        const int col = column(c, ((slot % WC) ^ swz_col<WC>(r)) * 8);
+        w_off[q] = col >= 0 ? (uint32_t)(r * (int)w_row + (col - c.n0) * 2) : kOutside;
       }
     } else {
-      w_base = (const uint8_t*)p.w + ((int64_t)c.g * p.n + c.n0) * w_row;
+      w_at = (const uint8_t*)p.w + ((int64_t)c.g * p.n + c.n0) * w_row;
       w_left = (p.n - c.n0) * w_row;
+      w_tail = (int)w_row;
 #pragma unroll
       for (int q = 0; q < WI; ++q) {
-        const int64_t col = column(c, q * (NT / WC) + tid / WC);
-        w_off[q] = col >= 0 ? (uint32_t)((col - c.n0) * w_row + w_ch * 16) : kOutside;
+        const int col = column(c, q * (NT / WC) + tid / WC);
+        w_off[q] = col >= 0 ? (uint32_t)(col - c.n0) * (uint32_t)w_row + w_ch : kOutside;
       }
     }
     if constexpr (MX) {
-      // scales of row `tid` (the first XW waves) or column tid - XW * 64; a
-      // row's scales begin at a whole dword, or (k % 128 == 64, odd rows) two
-      // bytes after one, and are then read from that dword on
-      xs_base = p.xs + c.m0 * s_row;
-      ws_base = p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
-      int64_t off = -1;
-      const uint8_t* base = x_scales ? xs_base : ws_base;
-      if (x_scales) {
-        if (tid < c.valid) off = tid * s_row;
-      } else if (tid - XW * 64 < BN) {
-        const int64_t col = column(c, tid - XW * 64);
-        if (col >= 0) off = (col - c.n0) * s_row;
+      if (any_scales) {
+        const uint8_t* base = x_scales ? p.xs + c.m0 * s_row : p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
+        const uint8_t* end = x_scales ? p.xs + p.m * s_row : p.ws + (int64_t)p.e * p.n * s_row;
+        const int64_t fine = (uintptr_t)base & 3;
+        s_at = base - fine;
+        // up to the end of the dword that holds the last scale (a dword that
+        // the descriptor cuts would read as zero)
+        s_left = ((end - s_at) + 3) & ~(int64_t)3;
+        const int row = x_scales ? (tid < c.valid ? tid : -1) : column(c, tid - XW * 64) - (int)c.n0;
+        const bool in = x_scales ? row >= 0 : column(c, tid - XW * 64) >= 0;
+        s_off = in ? ((uint32_t)row * (uint32_t)s_row + (uint32_t)fine) & ~3u : kOutside;
       }
-      const int fine = (int)(((uintptr_t)base + off) & 3);
-      s_odd = fine != 0 ? 1u : 0u;
-      // relative to the base rounded down to a dword
-      s_off = off >= 0 ? (uint32_t)(off - fine + ((uintptr_t)base & 3)) : kOutside;
     }
   };
-  // copies of k-step kt of the stream's tile into stage `st`; slot: for its
-  // scales when the step begins a group of them
+  // copies of the stream's next step (step kt of its tile) into stage `st`;
+  // slot: for its scales when the step begins a group of them
   auto issue = [&](bool live, int kt, int st, int slot) {
     if constexpr (MX) {
-      if (kt % SPG == 0) {
-        const bool mine = x_scales || wave < XW + BN / 64;
-        if (mine) {
-          const uint8_t* base = x_scales ? xs_base : ws_base;
-          const uint8_t* end = x_scales ? p.xs + p.m * s_row : p.ws + (int64_t)p.e * p.n * s_row;
-          const uint8_t* from = (const uint8_t*)((uintptr_t)base & ~(uintptr_t)3) + (kt / SPG) * 16;
-          // up to the end of the dword that holds the last scale (a dword
-          // that the descriptor cuts reads as zero)
-          const v4i r = buffer(from, live ? ((end - from) + 3) & ~(int64_t)3 : 0);
-          copy16(r, s_off, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc[slot * SROWS + wave * 64])));
-          if (s_row & 3) {
-            copy4(r, s_off + 16, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc2[slot * SROWS + wave * 64])));
-            odd_slots = (odd_slots & ~(1u << slot)) | s_odd << slot;
-          }
-        }
+      if (any_scales && kt % SPG == 0) {
+        const v4i r = buffer(s_at, live ? s_left : 0);
+        copy16(r, s_off, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc[slot * SROWS + wave * 64])));
+        if (s_split)
+          copy4(r, s_off == kOutside ? kOutside : s_off + 16,
+                __builtin_amdgcn_readfirstlane(lds_addr(&s_sc2[slot * SROWS + wave * 64])));
+        s_at += 16;
+        s_left -= 16;
       }
     }
-    const int64_t xa = XCOL ? (int64_t)kt * BK * x_row : (int64_t)kt * (BK * XBITS / 8);
-    const int64_t wa = WCOL ? (int64_t)kt * BK * w_row : (int64_t)kt * (BK * WBITS / 8);
-    const v4i xr = buffer(x_base + xa, live ? x_left - xa : 0), wr = buffer(w_base + wa, live ? w_left - wa : 0);
+    const v4i xr = buffer(x_at, live ? x_left : 0), wr = buffer(w_at, live ? w_left : 0);
     // the last step of a reduction that is no multiple of BK: chunks past the
     // row's end would be the next row's
-    const int64_t xe = XCOL ? 0 : x_row - xa, we = WCOL ? 0 : w_row - wa;
-    const bool x_in = XCOL || x_ch * 16 < xe, w_in = WCOL || w_ch * 16 < we;
+    constexpr int X_STEP = BK * XBITS / 8, W_STEP = BK * WBITS / 8;
+    const bool x_in = XCOL || x_ch < x_tail, w_in = WCOL || w_ch < w_tail;
+    const uint32_t xl = __builtin_amdgcn_readfirstlane(lds_addr(sX)) + st * X_BYTES + wave * 1024;
+    const uint32_t wl = __builtin_amdgcn_readfirstlane(lds_addr(sW)) + st * W_BYTES + wave * 1024;
 #pragma unroll
-    for (int q = 0; q < XI; ++q)
-      copy16(xr, x_in ? x_off[q] : kOutside,
-             __builtin_amdgcn_readfirstlane(lds_addr(sX + st * X_BYTES + (q * NWAVES + wave) * 1024)));
+    for (int q = 0; q < XI; ++q) copy16(xr, x_in ? x_off[q] : kOutside, xl + q * NWAVES * 1024);
 #pragma unroll
-    for (int q = 0; q < WI; ++q)
-      copy16(wr, w_in ? w_off[q] : kOutside,
-             __builtin_amdgcn_readfirstlane(lds_addr(sW + st * W_BYTES + (q * NWAVES + wave) * 1024)));
+    for (int q = 0; q < WI; ++q) copy16(wr, w_in ? w_off[q] : kOutside, wl + q * NWAVES * 1024);
+    const int64_t xd = XCOL ? BK * x_row : X_STEP, wd = WCOL ? BK * w_row : W_STEP;
+    x_at += xd;
+    x_left -= xd;
+    x_tail -= X_STEP;
+    w_at += wd;
+    w_left -= wd;
+    w_tail -= W_STEP;
   };
 
-  // ---- fragments of slice s of stage st.  A fragment holds 32 rows (x) or
-  // columns (w): lane l row l % 32, and its h = l / 32 half of the slice.
+  // ---- fragments.  A fragment holds 32 rows (x) or columns (w) of one slice:
+  // lane l row l % 32, and its h = l / 32 half of the slice.  The addresses of
+  // a lane, but for the stage, the fragment and the slice, are fixed.
   using Frag = std::conditional_t<MX, v8i, v8s>;
-  auto frag_rows = [&](const uint8_t* st, int row, int s, auto c_, auto bits_) -> Frag {
-    constexpr int C = decltype(c_)::value, BITS = decltype(bits_)::value;
-    const int z = swz_row<C>(row);
-    const uint8_t* a = st + row * (C * 16);
+  // rows along the reduction: pair u of chunks (chunk 2 u + h) of a row
+  constexpr int XU = XCOL ? FM : XC / 2, WU = WCOL ? FN : WC / 2;
+  uint32_t x_adr[XU], w_adr[WU];
+  auto row_adr = [&](int row, int u, auto c_) -> uint32_t {
+    constexpr int C = decltype(c_)::value;
+    return row * (C * 16) + (((2 * u + h) ^ swz_row<C>(row)) << 4);
+  };
+  // rows across it, by transposing reads: within 16 lanes, lane i receives
+  // element i % 16 of the four rows addressed by lanes 4 b .. 4 b + 3
+  // (b = 0..3, 4 elements each)
+  auto col_adr = [&](int first, auto c_) -> uint32_t {
+    constexpr int C = decltype(c_)::value;
+    const int i = lane & 15, grp = lane >> 4;
+    const int r = (grp >> 1) * 8 + (i >> 2), col = first + (grp & 1) * 16 + (i & 3) * 4;
+    return r * (C * 16) + ((((col >> 3) ^ swz_col<C>(r)) << 4) | ((col & 7) << 1));
+  };
+#pragma unroll
+  for (int u = 0; u < XU; ++u)
+    x_adr[u] = lds_addr(sX) + (XCOL ? col_adr(wm * WTM + u * 32, std::integral_constant<int, XCOL ? XC : 16>{})
+                                    : row_adr(wm * WTM + (lane & 31), u, std::integral_constant<int, XCOL ? 8 : XC>{}));
+#pragma unroll
+  for (int u = 0; u < WU; ++u)
+    w_adr[u] = lds_addr(sW) + (WCOL ? col_adr(wn * WTN + u * 32, std::integral_constant<int, WCOL ? WC : 16>{})
+                                    : row_adr(wn * WTN + (lane & 31), u, std::integral_constant<int, WCOL ? 8 : WC>{}));
+  auto lds4 = [](uint32_t a) -> v4i { return *(const LDS_PTR(v4i))a; };
+  auto frag_row = [&](uint32_t a0, uint32_t a1, auto bits_) -> Frag {
+    constexpr int BITS = decltype(bits_)::value;
+    const v4i lo = lds4(a0);
     if constexpr (!MX) {
-      return *(const LDS_PTR(v8s))(a + (((2 * s + h) ^ z) << 4));
-    } else if constexpr (BITS == 4) {
-      const v4i v = *(const LDS_PTR(v4i))(a + (((2 * s + h) ^ z) << 4));
-      return v8i{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      return __builtin_bit_cast(v8s, lo);
     } else {
-      const v4i lo = *(const LDS_PTR(v4i))(a + (((4 * s + h) ^ z) << 4));
-      const v4i hi = *(const LDS_PTR(v4i))(a + (((4 * s + 2 + h) ^ z) << 4));
+      const v4i hi = BITS == 8 ? lds4(a1) : v4i{0, 0, 0, 0};
       return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     }
   };
-  // transposing read: within 16 lanes, lane i receives element i % 16 of the
-  // four rows addressed by lanes 4 b .. 4 b + 3 (b = 0..3, 4 elements each)
-  auto frag_cols = [&](const uint8_t* st, int first, int s, auto c_) -> v8s {
-    constexpr int C = decltype(c_)::value;
-    const int i = lane & 15, grp = lane >> 4;
-    const int r = s * 16 + (grp >> 1) * 8 + (i >> 2), col = first + (grp & 1) * 16 + (i & 3) * 4;
-    const uint8_t* a = st + r * (C * 16) + ((((col >> 3) ^ swz_col<C>(r)) << 4) | ((col & 7) << 1));
+  auto frag_col = [&](uint32_t a, int row_bytes) -> v8s {
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(v4s))a);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(v4s))(a + 4 * C * 16));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR(v4s))(a + 4 * row_bytes));
     return v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   };
+  // s: the slice (a constant once unrolled; the wave's own with KWAVES)
   auto read_frags = [&](int st, int s, Frag (&xf)[FM], Frag (&wf)[FN]) {
-    const uint8_t* xb = sX + st * X_BYTES;
-    const uint8_t* wb = sW + st * W_BYTES;
+    constexpr int XP = XBITS == 8 ? 2 : 1;  // chunk pairs of a slice
+    const uint32_t xs = st * X_BYTES, ws = st * W_BYTES;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if constexpr (XCOL) xf[i] = frag_cols(xb, wm * WTM + i * 32, s, std::integral_constant<int, XC>{});
-      else xf[i] = frag_rows(xb, wm * WTM + i * 32 + (lane & 31), s, std::integral_constant<int, XC>{},
-                             std::integral_constant<int, XBITS>{});
+      if constexpr (XCOL) {
+        xf[i] = frag_col(x_adr[i] + xs + s * (16 * XC * 16), XC * 16);
+      } else if constexpr (KWAVES) {
+        const int row = i * 32 + (lane & 31);
+        constexpr auto c = std::integral_constant<int, XCOL ? 8 : XC>{};
+        xf[i] = frag_row(lds_addr(sX) + xs + row_adr(row, s * XP, c), lds_addr(sX) + xs + row_adr(row, s * XP + XP - 1, c),
+                         std::integral_constant<int, XBITS>{});
+      } else {
+        xf[i] = frag_row(x_adr[s * XP] + xs + i * (32 * XC * 16), x_adr[s * XP + XP - 1] + xs + i * (32 * XC * 16),
+                         std::integral_constant<int, XBITS>{});
+      }
     }
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      if constexpr (WCOL) wf[j] = frag_cols(wb, wn * WTN + j * 32, s, std::integral_constant<int, WC>{});
-      else wf[j] = frag_rows(wb, wn * WTN + j * 32 + (lane & 31), s, std::integral_constant<int, WC>{},
-                             std::integral_constant<int, WBITS>{});
-    }
-  };
-  // this step's scale bytes, one register a fragment: byte b is slice b's
-  uint32_t xsc[FM], wsc[FN];
-  auto read_scales = [&](int kt, int slot) {
-    if constexpr (MX) {
-      const int q0 = (kt % SPG) * NS;  // first slice of the step among the group's eight
-      const int shift = KWAVES ? 8 * ((q0 + wave) & 3) : 8 * (q0 & 3), word = (KWAVES ? q0 + wave : q0) >> 2;
-      const uint32_t* base = (const uint32_t*)&s_sc[slot * SROWS] + h * 2 + word;
-#pragma unroll
-      for (int i = 0; i < FM; ++i) xsc[i] = base[(wm * WTM + i * 32 + (lane & 31)) * 4] >> shift;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) wsc[j] = base[(XW * 64 + wn * WTN + j * 32 + (lane & 31)) * 4] >> shift;
-    }
-  };
-  // a landed group of scales, in place and by the thread that copied it: bytes of even
-  // blocks (the lanes with h = 0) and odd ones set apart; blocks past k become
-  // zero bytes (2^-127, never the NaN a neighbouring row may hold)
-  auto sort_scales = [&](int kt, int slot) {
-    if constexpr (MX) {
-      if (x_scales || wave < XW + BN / 64) {
-        v4u v = s_sc[slot * SROWS + wave * 64 + lane];
-        if (s_row & 3) {
-          const uint32_t next = s_sc2[slot * SROWS + wave * 64 + lane];
-          if ((odd_slots >> slot) & 1u)
-            v = v4u{__builtin_amdgcn_alignbyte(v.y, v.x, 2), __builtin_amdgcn_alignbyte(v.z, v.y, 2),
-                    __builtin_amdgcn_alignbyte(v.w, v.z, 2), __builtin_amdgcn_alignbyte(next, v.w, 2)};
-        }
-        const int pairs = (int)min((int64_t)8, (s_row - (int64_t)(kt / SPG) * 16) / 2);
-        const uint64_t keep = pairs >= 8 ? ~0ull : (1ull << (8 * pairs)) - 1;
-        const uint32_t k0 = (uint32_t)keep, k1 = (uint32_t)(keep >> 32);
-        s_sc[slot * SROWS + wave * 64 + lane] =
-            v4u{__builtin_amdgcn_perm(v.y, v.x, 0x06040200u) & k0, __builtin_amdgcn_perm(v.w, v.z, 0x06040200u) & k1,
-                __builtin_amdgcn_perm(v.y, v.x, 0x07050301u) & k0, __builtin_amdgcn_perm(v.w, v.z, 0x07050301u) & k1};
+      if constexpr (WCOL) {
+        wf[j] = frag_col(w_adr[j] + ws + s * (16 * WC * 16), WC * 16);
+      } else if constexpr (KWAVES) {
+        const uint32_t a = lds_addr(sW) + ws + row_adr(j * 32 + (lane & 31), s, std::integral_constant<int, WCOL ? 8 : WC>{});
+        wf[j] = frag_row(a, a, std::integral_constant<int, WBITS>{});
+      } else {
+        wf[j] = frag_row(w_adr[s] + ws + j * (32 * WC * 16), w_adr[s] + ws + j * (32 * WC * 16),
+                         std::integral_constant<int, WBITS>{});
       }
+    }
+  };
+  // This step's scales, one register a fragment.  Slice q of a group takes its
+  // blocks 2 q (lanes with h = 0) and 2 q + 1: of a step's bytes each lane
+  // keeps every second one.  With four slices a step byte s is slice s's, with
+  // two it is byte 2 s.  Blocks past k become zero bytes (2^-127, where the
+  // next row's may be a NaN).
+  uint32_t xsc[FM], wsc[FN];
+  auto read_scales = [&](const Tile& c, int kt, int slot) {
+    if constexpr (MX) {
+      const int left = ((int)p.k - kt * BK) / 64;  // slices of this step and after
+      const uint32_t odd_x = s_split ? (uint32_t)((c.m0 + lane) & 1) * 16 : 0, odd_w = s_split ? (uint32_t)(lane & 1) * 16 : 0;
+      auto one = [&](int row, uint32_t odd) -> uint32_t {
+        const uint32_t* words = (const uint32_t*)&s_sc[slot * SROWS + row];
+        if constexpr (KWAVES) {
+          const int at = 2 * ((kt % SPG) * NS + wave) + h + (int)(odd >> 3);
+          const uint8_t* b = at < 16 ? (const uint8_t*)words + at : (const uint8_t*)&s_sc2[slot * SROWS + row] + (at - 16);
+          const uint32_t v = *b;
+          return wave < left ? v : 0u;
+        } else if constexpr (NS == 4) {
+          const int w = (kt % SPG) * 2;
+          uint32_t d0 = words[w], d1 = words[w + 1];
+          if (s_split) {
+            const uint32_t d2 = w == 0 ? words[2] : s_sc2[slot * SROWS + row];
+            d0 = __builtin_amdgcn_alignbit(d1, d0, odd);
+            d1 = __builtin_amdgcn_alignbit(d2, d1, odd);
+          }
+          uint32_t v = __builtin_amdgcn_perm(d1, d0, h ? 0x07050301u : 0x06040200u);
+          if (left < 4) v &= (1u << (8 * left)) - 1;
+          return v;
+        } else {
+          const int w = kt % SPG;
+          uint32_t d0 = words[w];
+          if (s_split) d0 = __builtin_amdgcn_alignbit(w < 3 ? words[w + 1] : s_sc2[slot * SROWS + row], d0, odd);
+          uint32_t v = d0 >> (8 * h);
+          if (left < 2) v &= 0xFFu;
+          return v;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xsc[i] = one(wm * WTM + i * 32 + (lane & 31), odd_x);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + wn * WTN + j * 32 + (lane & 31), odd_w);
     }
   };
 
   v16f acc[FM][FN];
   auto multiply = [&](Frag (&xf)[FM], Frag (&wf)[FN], auto s_) {
-    constexpr int S = decltype(s_)::value & 3;
+    constexpr int S = KWAVES ? 0 : decltype(s_)::value * (NS == 4 ? 1 : 2);  // byte of the scale registers
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -520,22 +556,21 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, wf[j]),
                                                              __builtin_bit_cast(v8h, xf[i]), acc[i][j], 0, 0, 0);
         else
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf[i], acc[i][j], 4, ENC == kFp4 ? 4 : 0, S,
-                                                                      (int)wsc[j], S, (int)xsc[i]);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf[i], acc[i][j], 4, ENC == kFp4 ? 4 : 0,
+                                                                      S & 3, (int)wsc[j], S & 3, (int)xsc[i]);
       }
   };
 
   // ---- epilogue: lane l holds row l % 32 of each 32 x 32 block and columns
   // 8 (r / 4) + 4 h + r % 4, r = 0..15
-  const int64_t y_row = F;
-  auto store_block = [&](const Tile& c, int i, int col, const float (&v)[16]) {
-    const int row = wm * WTM + i * 32 + (lane & 31);
+  auto store_block = [&](const Tile& c, int lane, int i, int col, const float (&v)[16]) {
+    const int h = lane >> 5, row = wm * WTM + i * 32 + (lane & 31);
     if (row >= c.valid) return;
-    const int64_t at = (WGRAD ? (int64_t)c.g * p.k * p.n : 0) + (c.m0 + row) * y_row;
+    const int64_t at = (WGRAD ? (int64_t)c.g * p.k * p.n : 0) + (int64_t)(c.m0 + row) * F;
     if (p.out == kOutF32) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t n = c.n0 + col + 8 * q + 4 * h;
+        const int n = c.n0 + col + 8 * q + 4 * h;
         if (n >= F) continue;
         v4f o = v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         v4f* d = (v4f*)((float*)p.y + at + n);
@@ -564,12 +599,15 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         // row, so both are here.
         const auto a = __builtin_amdgcn_permlane32_swap(d[4 * q], d[4 * q + 2], false, false);
         const auto b = __builtin_amdgcn_permlane32_swap(d[4 * q + 1], d[4 * q + 3], false, false);
-        const int64_t n = c.n0 + col + 16 * q + 8 * h;
+        const int n = c.n0 + col + 16 * q + 8 * h;
         if (n < F) *(v4u*)((uint16_t*)p.y + at + n) = v4u{a[0], b[0], a[1], b[1]};
       }
     }
   };
-  auto epilogue = [&](const Tile& c) {
+  // Returns whether every lane issued every store (a tile without a rest).
+  auto epilogue = [&](const Tile& c) -> bool {
+    int lane = threadIdx.x & 63;  // opaque, as in set_sources
+    asm volatile("" : "+v"(lane));
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if constexpr (GLU) {
@@ -578,10 +616,12 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           float v[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
+            // u / (1 + 2^(-u log2 e)) * v with the hardware's 2^x and 1/x, each
+            // within 1 ulp; the rounded exponent adds |u| 2^-24
             const float u = acc[i][j][r];
-            v[r] = u / (1.0f + expf(-u)) * acc[i][j + 1][r];
+            v[r] = u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f)) * acc[i][j + 1][r];
           }
-          store_block(c, i, (wn * WTN + j * 32) / 2, v);
+          store_block(c, lane, i, (wn * WTN + j * 32) / 2, v);
         }
       } else {
 #pragma unroll
@@ -589,10 +629,11 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           float v[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
-          store_block(c, i, wn * WTN + j * 32, v);
+          store_block(c, lane, i, wn * WTN + j * 32, v);
         }
       }
     }
+    return c.valid == BM && c.n0 + (GLU ? BN / 2 : BN) <= F && !(WGRAD && p.accumulate);
   };
   auto clear = [&]() {
 #pragma unroll
@@ -606,9 +647,11 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   if (t0 < 0) return;
   int jl = 0, lk = 0, sc_in = 0;  // copies: tile count, k-step in it, slot of the next scales
   bool live = true;
-  Tile lc = coord(t0);
-  int lsteps = steps_of(lc);
-  set_sources(lc);
+  int lsteps;
+  Tile c = coord(t0);
+  int steps = steps_of(c);
+  set_sources(c);
+  lsteps = steps;
   auto feed = [&](int st) {
     issue(live, lk, st, sc_in);
     if constexpr (MX) {
@@ -619,7 +662,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       if (live) {
         const int t = tile_at(++jl);
         if (t >= 0) {
-          lc = coord(t);
+          const Tile lc = coord(t);
           lsteps = steps_of(lc);
           set_sources(lc);
         } else {
@@ -631,55 +674,57 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) feed(s);
   int st = 0, slot = STAGES - 1;  // computing: stage, slot of the scales in use
-  int kt = 0, jc = 0;
-  Tile c = coord(t0);
-  int steps = steps_of(c);
-  // the step `nk` of the computing stream has landed (its copies and all
-  // before them): sort its scales if it begins a group of them, and publish
-  auto publish = [&](int nk) {
-    wait_vmcnt<(STAGES - 2) * STEP_COPIES>();
-    if constexpr (MX) {
-      if (nk % SPG == 0) {
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
-        sort_scales(nk, slot);
-      }
-    }
+  int jc = 0;
+  // Step `nk` of the computing stream has landed (its copies and all before
+  // them): publish it.  After a tile whose stores were all issued, those
+  // stores, younger than the awaited copies, may stay in flight.
+  constexpr int YOUNGER = (STAGES - 2) * STEP_COPIES, BLOCKS = FM * FN / (GLU ? 2 : 1);
+  auto publish = [&](int nk, bool stored) {
+    if (stored && p.out == kOutF32) wait_vmcnt<(YOUNGER + BLOCKS * 4 < 63 ? YOUNGER + BLOCKS * 4 : 63)>();
+    else if (stored) wait_vmcnt<(YOUNGER + BLOCKS * 2 < 63 ? YOUNGER + BLOCKS * 2 : 63)>();
+    else wait_vmcnt<YOUNGER>();
+    if (MX && nk % SPG == 0) slot = slot + 1 == STAGES ? 0 : slot + 1;
     lds_barrier();
   };
   if constexpr (KWAVES) {
     while (true) {
       clear();
 #pragma unroll 1
-      for (kt = 0; kt < steps; ++kt) {
-        publish(kt);
+      for (int kt = 0; kt < steps; ++kt) {
+        publish(kt, false);
         feed(st == 0 ? STAGES - 1 : st - 1);
         Frag xf[FM], wf[FN];
-        read_scales(kt, slot);
+        read_scales(c, kt, slot);
         read_frags(st, wave, xf, wf);
         multiply(xf, wf, std::integral_constant<int, 0>{});
         st = st + 1 == STAGES ? 0 : st + 1;
       }
-      // the waves' sums meet in the first wave (its own first, then ascending)
-      if (wave > 0) {
+      // the waves' sums meet in the first wave: (0 + 2) + (1 + 3)
+      static_assert(!KWAVES || NWAVES == 4, "two rounds");
+      constexpr int Q = FM * FN * 4;
 #pragma unroll
-        for (int q = 0; q < FM * FN * 4; ++q) {
-          const v16f& a = acc[q / 4 / FN][q / 4 % FN];
-          s_sum[((wave - 1) * FM * FN * 4 + q) * 64 + lane] =
-              v4f{a[q % 4 * 4], a[q % 4 * 4 + 1], a[q % 4 * 4 + 2], a[q % 4 * 4 + 3]};
+      for (int round = 0; round < 2; ++round) {
+        const int half = round == 0 ? 2 : 1;  // waves half .. 2 half - 1 give, 0 .. half - 1 take
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const v16f& a = acc[q / 4 / FN][q / 4 % FN];
+            s_sum[((wave - half) * Q + q) * 64 + lane] =
+                v4f{a[q % 4 * 4], a[q % 4 * 4 + 1], a[q % 4 * 4 + 2], a[q % 4 * 4 + 3]};
+          }
         }
-      }
-      lds_barrier();
-      if (wave == 0) {
+        lds_barrier();
+        if (wave < half) {
 #pragma unroll
-        for (int w = 0; w < NWAVES - 1; ++w)
-#pragma unroll
-          for (int q = 0; q < FM * FN * 4; ++q) {
-            const v4f o = s_sum[(w * FM * FN * 4 + q) * 64 + lane];
+          for (int q = 0; q < Q; ++q) {
+            const v4f o = s_sum[(wave * Q + q) * 64 + lane];
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + r] += o[r];
           }
-        epilogue(c);
+        }
+        if (round == 0) lds_barrier();  // taken, before wave 1 gives in the same place
       }
+      if (wave == 0) epilogue(c);
       const int t = tile_at(++jc);
       if (t < 0) break;
       c = coord(t);
@@ -687,44 +732,56 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       // s_sum is written again only after the next tile's first barrier
     }
   } else {
-    static_assert(KWAVES || NS % 2 == 0, "fragment buffers alternate");
     Frag xf[2][FM], wf[2][FN];
-    publish(0);
-    read_scales(0, slot);
+    publish(0, false);
+    feed(STAGES - 1);
+    // a wave whose rows all lie past the group's last has nothing to multiply
+    bool alive = c.valid > wm * WTM, stored = false;
+    read_scales(c, 0, slot);
     read_frags(0, 0, xf[0], wf[0]);
     while (true) {
       clear();
-      int t_next = -1;
+      Tile next = c;
+      int t_next = 0;
 #pragma unroll 1
-      for (kt = 0; kt < steps; ++kt) {
-        // every wave has read the stage before this one: refill it
-        feed(st == 0 ? STAGES - 1 : st - 1);
-        static_for<NS - 1>([&](auto s_) {
-          constexpr int S = decltype(s_)::value;
-          read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
-          multiply(xf[S & 1], wf[S & 1], s_);
-        });
+      for (int kt = 0; kt < steps; ++kt) {
+        if (alive) {
+          static_for<NS - 1>([&](auto s_) {
+            constexpr int S = decltype(s_)::value;
+            read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+            multiply(xf[S & 1], wf[S & 1], s_);
+          });
+        }
+        const int old = st;
         st = st + 1 == STAGES ? 0 : st + 1;
         const bool last = kt + 1 == steps;
-        if (last) t_next = tile_at(++jc);
-        if (!last || t_next >= 0) {
-          // the next step's first fragments are read before this step's last
-          // products; its scales after them
-          publish(last ? 0 : kt + 1);
-          read_frags(st, 0, xf[0], wf[0]);
+        if (last) {
+          t_next = tile_at(++jc);
+          if (t_next >= 0) next = coord(t_next);
         }
-        multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{});
-        if (!last || t_next >= 0) read_scales(last ? 0 : kt + 1, slot);
+        const bool more = !last || t_next >= 0, alive_next = last ? next.valid > wm * WTM : alive;
+        if (more) {
+          // the next step is published, and every wave has read this one's
+          // stage: refill it; the next step's first fragments are read before
+          // this step's last products
+          publish(last ? 0 : kt + 1, stored);
+          stored = false;
+          feed(old);
+          if (alive_next) read_frags(st, 0, xf[0], wf[0]);
+        }
+        if (alive) multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{});
+        if (!last && alive) read_scales(c, kt + 1, slot);
       }
-      epilogue(c);
+      stored = epilogue(c);
       if (t_next < 0) break;
-      c = coord(t_next);
+      c = next;
       steps = steps_of(c);
+      alive = c.valid > wm * WTM;
+      if (alive) read_scales(c, 0, slot);
     }
   }
   wait_vmcnt<0>();  // no copy in flight when the workgroup ends
 }
-
 
 // ---------------------------------------------------------------- host side
 
@@ -895,6 +952,7 @@ template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU>
 void launch(const Plan& pl, hipStream_t s) {
   const size_t dyn = (size_t)(2 * pl.p.e + 1) * 4;
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
+  constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
   if (pl.kind == kLarge)
     hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, BK, 4, 2, 2, false, 2>), dim3(pl.grid),
                        dim3(512), dyn, s, pl.p);
@@ -902,7 +960,7 @@ void launch(const Plan& pl, hipStream_t s) {
     hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>), dim3(pl.grid),
                        dim3(256), dyn, s, pl.p);
   else if constexpr (!WGRAD)
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, 4, true, 2>), dim3(pl.grid),
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, STS, true, 2>), dim3(pl.grid),
                        dim3(256), dyn, s, pl.p);
 }
 
