@@ -93,11 +93,10 @@ __device__ __forceinline__ void copy4(v4i r, uint32_t off, uint32_t lds) {
                : "memory");
 }
 
-// A raw buffer over [base, base + bytes), bytes clamped to [0, 2^31].
-__device__ __forceinline__ v4i buffer(const void* base, int64_t bytes) {
+// A raw buffer over [base, base + bytes), bytes at most 2^31.
+__device__ __forceinline__ v4i buffer(const void* base, uint32_t bytes) {
   const int64_t b = uniform64((int64_t)base);
-  const int64_t n = bytes < 0 ? 0 : (bytes > (int64_t)kOutside ? (int64_t)kOutside : bytes);
-  return v4i{(int)b, (int)((b >> 32) & 0xFFFF), __builtin_amdgcn_readfirstlane((int)n), 0x00020000};
+  return v4i{(int)b, (int)((b >> 32) & 0xFFFF), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
 template <int N>
@@ -232,19 +231,28 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   static_assert((XCOL || NT / XC % 16 == 0) && (WCOL || NT / WC % 16 == 0), "one swizzle for all copies of a lane");
   constexpr int STEP_COPIES = XI + WI;
   static_assert((STAGES - 2) * STEP_COPIES < 64, "vmcnt range");
-  // E8M0 scales: 16 bytes a row at a time, the scales of 512 values
-  constexpr int SPG = MX ? 512 / BK : 1;  // k-steps of one group of scales
+  // E8M0 scales come a group at a time: with KWAVES 16 bytes a row (512
+  // values), by copies; else 32 bytes (1024 values) into the registers of the
+  // thread that looks after the row, which hands each step's on through LDS.
+  // (A row's bytes are a line of their own: the more of it a fetch takes, the
+  // less of the L2's path the scales need.  16 bytes a time cost a step of the
+  // 256-row FP4 tile 1000 of 5100 cycles.)
+  constexpr int SPG = MX ? (KWAVES ? 512 : 1024) / BK : 1;  // k-steps of one group of scales
   constexpr int XW = (BM + 63) / 64, SROWS = MX ? XW * 64 + BN : 1;  // rows whose scales are staged
-  static_assert(!MX || XW + BN / 64 <= NWAVES, "a thread for each row's scales");
+  static_assert(!MX || SROWS <= NT, "a thread for each row's scales");
+  constexpr int SB = BK / 128;  // words of a row's scales in one step
+  static_assert(!MX || KWAVES || (STAGES == 2 && (SB == 1 || SB == 2)), "scales are handed on a step ahead");
 
   __shared__ __attribute__((aligned(16))) uint8_t sX[STAGES * X_BYTES];
   __shared__ __attribute__((aligned(16))) uint8_t sW[STAGES * W_BYTES];
-  // groups of scales as they lie in memory, from the dword that holds a row's
-  // first one: up to STAGES - 1 in flight (a tile may end within a group) and
-  // the one in use.  s_sc2: the dword after the 16 bytes, for rows that begin
-  // in the middle of a dword.
-  __shared__ __attribute__((aligned(16))) v4u s_sc[MX ? STAGES * SROWS : 1];
-  __shared__ __attribute__((aligned(16))) uint32_t s_sc2[MX ? STAGES * SROWS : 1];
+  // KWAVES: groups of scales as they lie in memory, from the dword that holds a
+  // row's first one: up to STAGES - 1 in flight (a tile may end within a
+  // group) and the one in use.  s_sc2: the dword after the 16 bytes, for rows
+  // that begin in the middle of a dword.
+  __shared__ __attribute__((aligned(16))) v4u s_sc[MX && KWAVES ? STAGES * SROWS : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t s_sc2[MX && KWAVES ? STAGES * SROWS : 1];
+  // else: the scales of two steps, SB words a row
+  __shared__ __attribute__((aligned(16))) uint32_t s_step[MX && !KWAVES ? 2 * SROWS * SB : 1];
   __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? 2 * FM * FN * 4 * 64 : 1];
   extern __shared__ __attribute__((aligned(16))) int32_t s_dyn[];
   int32_t* s_ends = s_dyn;
@@ -311,7 +319,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   };
   auto steps_of = [&](const Tile& c) -> int {
     const int s = (int)(((int64_t)c.r1 - c.r0 + BK - 1) / BK);
-    return WGRAD ? max(s, 1) : s;  // an expert without rows: one step of zeros
+    return KWAVES ? s : max(s, 2);  // at least two in the pipeline below, of zeros if need be
   };
 
   // column of the weights for column q of the tile; -1 past the last
@@ -324,24 +332,29 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     }
   };
 
-  // ---- the copy stream's state: where the next step of its tile comes from
+  // ---- the copy stream's state: where the next step of its tile comes from.
+  // Sizes from there to the operand's end fit 32 bits: rows along the
+  // reduction are cut to the tile's, rows across it to one stage.
   const uint8_t* x_at = nullptr;
   const uint8_t* w_at = nullptr;
-  const uint8_t* s_at = nullptr;   // the row (first XW waves) or column scales, from a whole dword on
-  int64_t x_left = 0, w_left = 0, s_left = 0;  // bytes from there to the operand's end
-  int x_tail = 0, w_tail = 0;      // bytes from there to the end of a row along the reduction
-  uint32_t x_off[XI], w_off[WI], s_off = kOutside;
+  const uint8_t* xs_at = nullptr;  // the tile's row and column scales, from a whole dword on
+  const uint8_t* ws_at = nullptr;
+  uint32_t x_size = 0, w_size = 0, xs_size = 0, ws_size = 0;
+  int r_left = 0;                  // of the reduction, from the step on
+  uint32_t x_skip = 0, w_skip = 0; // rows across the reduction: bytes of a row before the tile
+  uint32_t x_off[XI], w_off[WI], s_off = kOutside, s_odd = 0;
   const int x_ch = XCOL ? 0 : ((lane % XC) ^ swz_row<XC>(tid / XC)) * 16;
   const int w_ch = WCOL ? 0 : ((lane % WC) ^ swz_row<WC>(tid / WC)) * 16;
-  const bool x_scales = wave < XW, any_scales = MX && wave < XW + BN / 64;
+  auto cut = [](int64_t bytes) -> uint32_t { return (uint32_t)(bytes > (int64_t)kOutside ? (int64_t)kOutside : bytes); };
   auto set_sources = [&](const Tile& c) {
     // indices pass through an opaque point: the offsets are computed here,
     // once a tile, and not kept in parts across the k-loop
     int lane = threadIdx.x & 63, tid = threadIdx.x;
     asm volatile("" : "+v"(lane), "+v"(tid));
+    r_left = c.r1 - c.r0;
     if constexpr (XCOL) {  // wgrad: from (first row of the group, first column of the tile)
-      x_at = (const uint8_t*)p.x + ((int64_t)c.r0 * p.k + c.m0) * 2;
-      x_left = (c.r1 - c.r0) * x_row - c.m0 * 2;
+      x_skip = c.m0 * 2;
+      x_at = (const uint8_t*)p.x + (int64_t)c.r0 * x_row + x_skip;
 #pragma unroll
       for (int q = 0; q < XI; ++q) {
         const int slot = q * NT + tid, r = slot / XC;
@@ -350,14 +363,13 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     } else {
       x_at = (const uint8_t*)p.x + c.m0 * x_row;
-      x_left = c.valid * x_row;
-      x_tail = (int)x_row;
+      x_size = c.valid * (uint32_t)x_row;
 #pragma unroll
       for (int q = 0; q < XI; ++q) x_off[q] = (uint32_t)((q * (NT / XC) + tid / XC) * (int)x_row + x_ch);
     }
     if constexpr (WCOL) {  // from the tile's first column, of the expert's first row (or the group's)
-      w_at = (const uint8_t*)p.w + ((WGRAD ? (int64_t)c.r0 : c.g * p.k) * p.n + c.n0) * 2;
-      w_left = (c.r1 - c.r0) * w_row - c.n0 * 2;
+      w_skip = c.n0 * 2;
+      w_at = (const uint8_t*)p.w + (WGRAD ? (int64_t)c.r0 : c.g * p.k) * w_row + w_skip;
 #pragma unroll
       for (int q = 0; q < WI; ++q) {
         const int slot = q * NT + tid, r = slot / WC;
@@ -366,8 +378,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     } else {
       w_at = (const uint8_t*)p.w + ((int64_t)c.g * p.n + c.n0) * w_row;
-      w_left = (p.n - c.n0) * w_row;
-      w_tail = (int)w_row;
+      w_size = cut((p.n - c.n0) * w_row);
 #pragma unroll
       for (int q = 0; q < WI; ++q) {
         const int col = column(c, q * (NT / WC) + tid / WC);
@@ -375,58 +386,114 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     }
     if constexpr (MX) {
-      if (any_scales) {
-        const uint8_t* base = x_scales ? p.xs + c.m0 * s_row : p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
-        const uint8_t* end = x_scales ? p.xs + p.m * s_row : p.ws + (int64_t)p.e * p.n * s_row;
-        const int64_t fine = (uintptr_t)base & 3;
-        s_at = base - fine;
-        // up to the end of the dword that holds the last scale (a dword that
-        // the descriptor cuts would read as zero)
-        s_left = ((end - s_at) + 3) & ~(int64_t)3;
-        const int row = x_scales ? (tid < c.valid ? tid : -1) : column(c, tid - XW * 64) - (int)c.n0;
-        const bool in = x_scales ? row >= 0 : column(c, tid - XW * 64) >= 0;
-        s_off = in ? ((uint32_t)row * (uint32_t)s_row + (uint32_t)fine) & ~3u : kOutside;
+      const uint8_t* xb = p.xs + c.m0 * s_row;
+      const uint8_t* wb = p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
+      const uint32_t xf = (uintptr_t)xb & 3, wf = (uintptr_t)wb & 3;
+      xs_at = xb - xf;
+      ws_at = wb - wf;
+      // up to the end of the dword that holds the last scale (a dword that the
+      // descriptor cuts would read as zero)
+      xs_size = cut((p.xs + p.m * s_row - xs_at + 3) & ~(int64_t)3);
+      ws_size = cut((p.ws + (int64_t)p.e * p.n * s_row - ws_at + 3) & ~(int64_t)3);
+      // of the staged rows: x first, then columns
+      const uint32_t from = tid < XW * 64 ? xf : wf;
+      const int row = tid < XW * 64 ? (tid < c.valid ? tid : -1) : (tid < SROWS ? column(c, tid - XW * 64) : -1);
+      const uint32_t at = (uint32_t)(tid < XW * 64 ? row : row - c.n0) * (uint32_t)s_row + from;
+      s_off = row >= 0 ? at & ~3u : kOutside;
+      s_odd = (at & 3) * 8;  // bits
+    }
+  };
+  // Copies of the stream's next step (step kt of its tile) into stage `st`:
+  // first its scales (into `slot`, when the step begins a group of them), then
+  // one copy after the other.  A copy keeps the CU's address path busy for 16
+  // to 21 cycles; all at once they block every wave in turn, so they are
+  // issued between the products.
+  typedef uint32_t v8u __attribute__((ext_vector_type(8)));
+  v8u sc_group;           // this thread's row: what is left of its group of scales, the next step's first
+  uint32_t sc_last = 0, sc_odd = 0;
+  int sc_blocks = 0;      // blocks of the step that exist
+  auto issue_scales = [&](int kt, int slot) {
+    if constexpr (MX) {
+      sc_blocks = min(BK, r_left) / 32;
+      if (kt % SPG == 0 && (SROWS == NT || wave * 64 < SROWS)) {
+        const v4i r = wave < XW ? buffer(xs_at, xs_size) : buffer(ws_at, ws_size);
+        if constexpr (KWAVES) {
+          const uint32_t at = kt / SPG * 16;
+          copy16(r, s_off + at, __builtin_amdgcn_readfirstlane(lds_addr(s_sc)) + (slot * SROWS + wave * 64) * 16);
+          if (s_split)
+            copy4(r, s_off + at + 16, __builtin_amdgcn_readfirstlane(lds_addr(s_sc2)) + (slot * SROWS + wave * 64) * 4);
+        } else {
+          const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+              (void*)(((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x), 0, r.z, 0x00020000);
+          const int at = (int)s_off + kt / SPG * 32;
+          const v4u lo = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
+          const v4u hi = __builtin_amdgcn_raw_buffer_load_b128(b, at + 16, 0, 0);
+          sc_group = v8u{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          sc_last = __builtin_amdgcn_raw_buffer_load_b32(b, at + 32, 0, 0);
+          sc_odd = s_odd;
+        }
       }
     }
   };
-  // copies of the stream's next step (step kt of its tile) into stage `st`;
-  // slot: for its scales when the step begins a group of them
-  auto issue = [&](bool live, int kt, int st, int slot) {
-    if constexpr (MX) {
-      if (any_scales && kt % SPG == 0) {
-        const v4i r = buffer(s_at, live ? s_left : 0);
-        copy16(r, s_off, __builtin_amdgcn_readfirstlane(lds_addr(&s_sc[slot * SROWS + wave * 64])));
-        if (s_split)
-          copy4(r, s_off == kOutside ? kOutside : s_off + 16,
-                __builtin_amdgcn_readfirstlane(lds_addr(&s_sc2[slot * SROWS + wave * 64])));
-        s_at += 16;
-        s_left -= 16;
+  // The coming step's scales, from the thread that holds its row's; blocks
+  // past k become zero bytes (2^-127, where the next row's may be a NaN).
+  auto hand_on = [&](int slot) {
+    if constexpr (MX && !KWAVES) {
+      if (SROWS == NT || wave * 64 < SROWS) {
+        uint32_t d[SB];
+#pragma unroll
+        for (int q = 0; q < SB; ++q) {
+          d[q] = __builtin_amdgcn_alignbit(sc_group[q + 1], sc_group[q], sc_odd);
+          const int bytes = sc_blocks - 4 * q;
+          if (bytes < 4) d[q] &= bytes <= 0 ? 0u : (1u << (8 * bytes)) - 1;
+        }
+        uint32_t* to = &s_step[(slot * SROWS + tid) * SB];
+        if constexpr (SB == 2) *(uint64_t*)to = (uint64_t)d[1] << 32 | d[0];
+        else *to = d[0];
+        if constexpr (SB == 2) sc_group = v8u{sc_group[2], sc_group[3], sc_group[4], sc_group[5], sc_group[6], sc_group[7], sc_last, 0};
+        else sc_group = v8u{sc_group[1], sc_group[2], sc_group[3], sc_group[4], sc_group[5], sc_group[6], sc_group[7], sc_last};
       }
     }
-    const v4i xr = buffer(x_at, live ? x_left : 0), wr = buffer(w_at, live ? w_left : 0);
-    // the last step of a reduction that is no multiple of BK: chunks past the
-    // row's end would be the next row's
-    constexpr int X_STEP = BK * XBITS / 8, W_STEP = BK * WBITS / 8;
-    const bool x_in = XCOL || x_ch < x_tail, w_in = WCOL || w_ch < w_tail;
-    const uint32_t xl = __builtin_amdgcn_readfirstlane(lds_addr(sX)) + st * X_BYTES + wave * 1024;
-    const uint32_t wl = __builtin_amdgcn_readfirstlane(lds_addr(sW)) + st * W_BYTES + wave * 1024;
-#pragma unroll
-    for (int q = 0; q < XI; ++q) copy16(xr, x_in ? x_off[q] : kOutside, xl + q * NWAVES * 1024);
-#pragma unroll
-    for (int q = 0; q < WI; ++q) copy16(wr, w_in ? w_off[q] : kOutside, wl + q * NWAVES * 1024);
-    const int64_t xd = XCOL ? BK * x_row : X_STEP, wd = WCOL ? BK * w_row : W_STEP;
-    x_at += xd;
-    x_left -= xd;
-    x_tail -= X_STEP;
-    w_at += wd;
-    w_left -= wd;
-    w_tail -= W_STEP;
+  };
+  auto across = [&](uint32_t row, uint32_t skip) -> uint32_t {  // size of one stage's rows
+    return r_left > 0 ? min(r_left, BK) * row - skip : 0u;
+  };
+  auto issue_copy = [&](int st, auto q_) {
+    constexpr int Q = decltype(q_)::value;
+    // in the last step of a reduction that is no multiple of BK, chunks past
+    // the row's end would be the next row's
+    if constexpr (Q < XI) {
+      const v4i xr = buffer(x_at, XCOL ? across((uint32_t)x_row, x_skip) : x_size);
+      copy16(xr, XCOL || x_ch * 8 / XBITS < r_left ? x_off[Q] : kOutside,
+             __builtin_amdgcn_readfirstlane(lds_addr(sX)) + st * X_BYTES + (Q * NWAVES + wave) * 1024);
+    } else {
+      const v4i wr = buffer(w_at, WCOL ? across((uint32_t)w_row, w_skip) : w_size);
+      copy16(wr, WCOL || w_ch * 8 / WBITS < r_left ? w_off[Q - XI] : kOutside,
+             __builtin_amdgcn_readfirstlane(lds_addr(sW)) + st * W_BYTES + ((Q - XI) * NWAVES + wave) * 1024);
+    }
+  };
+  auto advance = [&]() {
+    x_at += XCOL ? BK * x_row : BK * XBITS / 8;
+    w_at += WCOL ? BK * w_row : BK * WBITS / 8;
+    // (never below nothing: past the last tile zeros are still copied)
+    if constexpr (!XCOL) x_size = x_size > BK * XBITS / 8 ? x_size - BK * XBITS / 8 : 0;
+    if constexpr (!WCOL) w_size = w_size > BK * WBITS / 8 ? w_size - BK * WBITS / 8 : 0;
+    r_left = max(r_left - BK, 0);
+  };
+  auto no_sources = [&]() {
+    x_size = w_size = xs_size = ws_size = 0;
+    r_left = 0;
   };
 
   // ---- fragments.  A fragment holds 32 rows (x) or columns (w) of one slice:
   // lane l row l % 32, and its h = l / 32 half of the slice.  The addresses of
   // a lane, but for the stage, the fragment and the slice, are fixed.
-  using Frag = std::conditional_t<MX, v8i, v8s>;
+  using XFrag = std::conditional_t<ENC == kFp8, v8i, std::conditional_t<MX, v4i, v8s>>;
+  using WFrag = std::conditional_t<MX, v4i, v8s>;
+  auto wide = [](auto v) -> v8i {  // as the instruction's type takes it (FP4: the upper half is not read)
+    if constexpr (sizeof(v) == 32) return v;
+    else return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+  };
   // rows along the reduction: pair u of chunks (chunk 2 u + h) of a row
   constexpr int XU = XCOL ? FM : XC / 2, WU = WCOL ? FN : WC / 2;
   uint32_t x_adr[XU], w_adr[WU];
@@ -452,14 +519,13 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     w_adr[u] = lds_addr(sW) + (WCOL ? col_adr(wn * WTN + u * 32, std::integral_constant<int, WCOL ? WC : 16>{})
                                     : row_adr(wn * WTN + (lane & 31), u, std::integral_constant<int, WCOL ? 8 : WC>{}));
   auto lds4 = [](uint32_t a) -> v4i { return *(const LDS_PTR(v4i))a; };
-  auto frag_row = [&](uint32_t a0, uint32_t a1, auto bits_) -> Frag {
-    constexpr int BITS = decltype(bits_)::value;
+  auto frag_row = [&](uint32_t a0, uint32_t a1, auto* f) {
     const v4i lo = lds4(a0);
-    if constexpr (!MX) {
-      return __builtin_bit_cast(v8s, lo);
+    if constexpr (sizeof(*f) == 32) {
+      const v4i hi = lds4(a1);
+      *f = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     } else {
-      const v4i hi = BITS == 8 ? lds4(a1) : v4i{0, 0, 0, 0};
-      return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      *f = __builtin_bit_cast(std::remove_reference_t<decltype(*f)>, lo);
     }
   };
   auto frag_col = [&](uint32_t a, int row_bytes) -> v8s {
@@ -468,7 +534,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     return v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   };
   // s: the slice (a constant once unrolled; the wave's own with KWAVES)
-  auto read_frags = [&](int st, int s, Frag (&xf)[FM], Frag (&wf)[FN]) {
+  auto read_frags = [&](int st, int s, XFrag (&xf)[FM], WFrag (&wf)[FN]) {
     constexpr int XP = XBITS == 8 ? 2 : 1;  // chunk pairs of a slice
     const uint32_t xs = st * X_BYTES, ws = st * W_BYTES;
 #pragma unroll
@@ -478,11 +544,11 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       } else if constexpr (KWAVES) {
         const int row = i * 32 + (lane & 31);
         constexpr auto c = std::integral_constant<int, XCOL ? 8 : XC>{};
-        xf[i] = frag_row(lds_addr(sX) + xs + row_adr(row, s * XP, c), lds_addr(sX) + xs + row_adr(row, s * XP + XP - 1, c),
-                         std::integral_constant<int, XBITS>{});
+        const uint32_t at = lds_addr(sX) + xs;
+        frag_row(at + row_adr(row, s * XP, c), at + row_adr(row, s * XP + XP - 1, c), &xf[i]);
       } else {
-        xf[i] = frag_row(x_adr[s * XP] + xs + i * (32 * XC * 16), x_adr[s * XP + XP - 1] + xs + i * (32 * XC * 16),
-                         std::integral_constant<int, XBITS>{});
+        const uint32_t at = xs + i * (32 * XC * 16);
+        frag_row(x_adr[s * XP] + at, x_adr[s * XP + XP - 1] + at, &xf[i]);
       }
     }
 #pragma unroll
@@ -490,76 +556,74 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       if constexpr (WCOL) {
         wf[j] = frag_col(w_adr[j] + ws + s * (16 * WC * 16), WC * 16);
       } else if constexpr (KWAVES) {
-        const uint32_t a = lds_addr(sW) + ws + row_adr(j * 32 + (lane & 31), s, std::integral_constant<int, WCOL ? 8 : WC>{});
-        wf[j] = frag_row(a, a, std::integral_constant<int, WBITS>{});
+        frag_row(lds_addr(sW) + ws + row_adr(j * 32 + (lane & 31), s, std::integral_constant<int, WCOL ? 8 : WC>{}), 0, &wf[j]);
       } else {
-        wf[j] = frag_row(w_adr[s] + ws + j * (32 * WC * 16), w_adr[s] + ws + j * (32 * WC * 16),
-                         std::integral_constant<int, WBITS>{});
+        frag_row(w_adr[s] + ws + j * (32 * WC * 16), 0, &wf[j]);
       }
     }
   };
-  // This step's scales, one register a fragment.  Slice q of a group takes its
+  // This step's scales, one register a fragment.  Slice q of a step takes its
   // blocks 2 q (lanes with h = 0) and 2 q + 1: of a step's bytes each lane
-  // keeps every second one.  With four slices a step byte s is slice s's, with
-  // two it is byte 2 s.  Blocks past k become zero bytes (2^-127, where the
-  // next row's may be a NaN).
+  // keeps every second one.  With four slices byte s is slice s's, with two it
+  // is byte 2 s.
   uint32_t xsc[FM], wsc[FN];
   auto read_scales = [&](const Tile& c, int kt, int slot) {
-    if constexpr (MX) {
-      const int left = ((int)p.k - kt * BK) / 64;  // slices of this step and after
-      const uint32_t odd_x = s_split ? (uint32_t)((c.m0 + lane) & 1) * 16 : 0, odd_w = s_split ? (uint32_t)(lane & 1) * 16 : 0;
+    if constexpr (MX && KWAVES) {
+      const bool in = kt * BK + wave * 64 < (int)p.k;  // this wave's slice exists
       auto one = [&](int row, uint32_t odd) -> uint32_t {
-        const uint32_t* words = (const uint32_t*)&s_sc[slot * SROWS + row];
-        if constexpr (KWAVES) {
-          const int at = 2 * ((kt % SPG) * NS + wave) + h + (int)(odd >> 3);
-          const uint8_t* b = at < 16 ? (const uint8_t*)words + at : (const uint8_t*)&s_sc2[slot * SROWS + row] + (at - 16);
-          const uint32_t v = *b;
-          return wave < left ? v : 0u;
-        } else if constexpr (NS == 4) {
-          const int w = (kt % SPG) * 2;
-          uint32_t d0 = words[w], d1 = words[w + 1];
-          if (s_split) {
-            const uint32_t d2 = w == 0 ? words[2] : s_sc2[slot * SROWS + row];
-            d0 = __builtin_amdgcn_alignbit(d1, d0, odd);
-            d1 = __builtin_amdgcn_alignbit(d2, d1, odd);
-          }
-          uint32_t v = __builtin_amdgcn_perm(d1, d0, h ? 0x07050301u : 0x06040200u);
-          if (left < 4) v &= (1u << (8 * left)) - 1;
-          return v;
+        const int at = 2 * ((kt % SPG) * NS + wave) + h + (int)odd;
+        const uint8_t* b = at < 16 ? (const uint8_t*)&s_sc[slot * SROWS + row] + at
+                                   : (const uint8_t*)&s_sc2[slot * SROWS + row] + (at - 16);
+        const uint32_t v = *b;
+        return in ? v : 0u;
+      };
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xsc[i] = one(i * 32 + (lane & 31), s_split ? ((c.m0 + lane) & 1) * 2 : 0);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + j * 32 + (lane & 31), s_split ? (lane & 1) * 2 : 0);
+    } else if constexpr (MX) {
+      auto one = [&](int row) -> uint32_t {
+        const uint32_t* words = &s_step[(slot * SROWS + row) * SB];
+        if constexpr (SB == 2) {
+          const uint64_t two = *(const uint64_t*)words;
+          return __builtin_amdgcn_perm((uint32_t)(two >> 32), (uint32_t)two, h ? 0x07050301u : 0x06040200u);
         } else {
-          const int w = kt % SPG;
-          uint32_t d0 = words[w];
-          if (s_split) d0 = __builtin_amdgcn_alignbit(w < 3 ? words[w + 1] : s_sc2[slot * SROWS + row], d0, odd);
-          uint32_t v = d0 >> (8 * h);
-          if (left < 2) v &= 0xFFu;
-          return v;
+          return *words >> (8 * h);
         }
       };
 #pragma unroll
-      for (int i = 0; i < FM; ++i) xsc[i] = one(wm * WTM + i * 32 + (lane & 31), odd_x);
+      for (int i = 0; i < FM; ++i) xsc[i] = one(wm * WTM + i * 32 + (lane & 31));
 #pragma unroll
-      for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + wn * WTN + j * 32 + (lane & 31), odd_w);
+      for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + wn * WTN + j * 32 + (lane & 31));
     }
   };
 
   v16f acc[FM][FN];
-  auto multiply = [&](Frag (&xf)[FM], Frag (&wf)[FN], auto s_) {
+  // between(m): what is issued after product m of the slice
+  auto multiply = [&](XFrag (&xf)[FM], WFrag (&wf)[FN], auto s_, auto between) {
     constexpr int S = KWAVES ? 0 : decltype(s_)::value * (NS == 4 ? 1 : 2);  // byte of the scale registers
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        if constexpr (ENC == kBf16)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, wf[j]),
-                                                              __builtin_bit_cast(v8bf, xf[i]), acc[i][j], 0, 0, 0);
-        else if constexpr (ENC == kF16)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, wf[j]),
-                                                             __builtin_bit_cast(v8h, xf[i]), acc[i][j], 0, 0, 0);
-        else
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf[i], acc[i][j], 4, ENC == kFp4 ? 4 : 0,
-                                                                      S & 3, (int)wsc[j], S & 3, (int)xsc[i]);
-      }
+    static_for<FM * FN>([&](auto m_) {
+      constexpr int i = decltype(m_)::value / FN, j = decltype(m_)::value % FN;
+      if constexpr (ENC == kBf16)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, wf[j]),
+                                                            __builtin_bit_cast(v8bf, xf[i]), acc[i][j], 0, 0, 0);
+      else if constexpr (ENC == kF16)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, wf[j]),
+                                                           __builtin_bit_cast(v8h, xf[i]), acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(wf[j]), wide(xf[i]), acc[i][j], 4, ENC == kFp4 ? 4 : 0, S & 3,
+                                                                    (int)wsc[j], S & 3, (int)xsc[i]);
+      between(m_);
+    });
+    // The sums are needed here as far as the compiler can tell: it would move
+    // the products of a whole step behind the next branch, past the barrier,
+    // with the fragments of all its slices held until then.
+    static_for<FM * FN>([&](auto m_) {
+      v16f& a = acc[decltype(m_)::value / FN][decltype(m_)::value % FN];
+      asm volatile("" : "+v"(a));
+    });
   };
+  auto nothing = [](auto) {};
 
   // ---- epilogue: lane l holds row l % 32 of each 32 x 32 block and columns
   // 8 (r / 4) + 4 h + r % 4, r = 0..15
@@ -642,61 +706,57 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       for (int j = 0; j < FN; ++j) acc[i][j] = v16f{0};
   };
 
-  // ---- the two streams
   const int t0 = tile_at(0);
   if (t0 < 0) return;
-  int jl = 0, lk = 0, sc_in = 0;  // copies: tile count, k-step in it, slot of the next scales
-  bool live = true;
-  int lsteps;
   Tile c = coord(t0);
-  int steps = steps_of(c);
+  int steps = steps_of(c), jc = 0;
+  int st = 0, slot = KWAVES ? STAGES - 1 : 0;  // computing: stage, slot of the scales in use
   set_sources(c);
-  lsteps = steps;
-  auto feed = [&](int st) {
-    issue(live, lk, st, sc_in);
-    if constexpr (MX) {
-      if (lk % SPG == 0) sc_in = sc_in + 1 == STAGES ? 0 : sc_in + 1;
-    }
-    if (++lk == lsteps) {
-      lk = 0;
-      if (live) {
+  // A step of the computing stream has landed (its copies and all before
+  // them): publish it.
+  constexpr int YOUNGER = (STAGES - 2) * STEP_COPIES;
+
+  if constexpr (KWAVES) {
+    // A stream of copies STAGES - 1 steps ahead that crosses the tiles' borders
+    int jl = 0, lk = 0, lsteps = steps, sc_in = 0;  // tile count, k-step in it, slot of the next scales
+    bool live = true;
+    auto feed = [&](int st) {
+      issue_scales(lk, sc_in);
+      if constexpr (MX) {
+        if (lk % SPG == 0) sc_in = sc_in + 1 == STAGES ? 0 : sc_in + 1;
+      }
+      static_for<STEP_COPIES>([&](auto q_) { issue_copy(st, q_); });
+      advance();
+      if (++lk == lsteps && live) {
+        lk = 0;
         const int t = tile_at(++jl);
-        if (t >= 0) {
+        live = t >= 0;
+        if (live) {
           const Tile lc = coord(t);
           lsteps = steps_of(lc);
           set_sources(lc);
         } else {
-          live = false;  // what is still issued copies zeros
+          no_sources();  // what is still issued copies zeros
         }
       }
-    }
-  };
+    };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) feed(s);
-  int st = 0, slot = STAGES - 1;  // computing: stage, slot of the scales in use
-  int jc = 0;
-  // Step `nk` of the computing stream has landed (its copies and all before
-  // them): publish it.  After a tile whose stores were all issued, those
-  // stores, younger than the awaited copies, may stay in flight.
-  constexpr int YOUNGER = (STAGES - 2) * STEP_COPIES, BLOCKS = FM * FN / (GLU ? 2 : 1);
-  auto publish = [&](int nk, bool stored) {
-    if (stored && p.out == kOutF32) wait_vmcnt<(YOUNGER + BLOCKS * 4 < 63 ? YOUNGER + BLOCKS * 4 : 63)>();
-    else if (stored) wait_vmcnt<(YOUNGER + BLOCKS * 2 < 63 ? YOUNGER + BLOCKS * 2 : 63)>();
-    else wait_vmcnt<YOUNGER>();
-    if (MX && nk % SPG == 0) slot = slot + 1 == STAGES ? 0 : slot + 1;
-    lds_barrier();
-  };
-  if constexpr (KWAVES) {
+    for (int s = 0; s < STAGES - 1; ++s) feed(s);
     while (true) {
       clear();
 #pragma unroll 1
       for (int kt = 0; kt < steps; ++kt) {
-        publish(kt, false);
+        wait_vmcnt<YOUNGER>();
+        if constexpr (MX) {
+          if (kt % SPG == 0) slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
+        lds_barrier();
         feed(st == 0 ? STAGES - 1 : st - 1);
-        Frag xf[FM], wf[FN];
+        XFrag xf[FM];
+        WFrag wf[FN];
         read_scales(c, kt, slot);
         read_frags(st, wave, xf, wf);
-        multiply(xf, wf, std::integral_constant<int, 0>{});
+        multiply(xf, wf, std::integral_constant<int, 0>{}, nothing);
         st = st + 1 == STAGES ? 0 : st + 1;
       }
       // the waves' sums meet in the first wave: (0 + 2) + (1 + 3)
@@ -732,52 +792,84 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       // s_sum is written again only after the next tile's first barrier
     }
   } else {
-    Frag xf[2][FM], wf[2][FN];
-    publish(0, false);
-    feed(STAGES - 1);
-    // a wave whose rows all lie past the group's last has nothing to multiply
-    bool alive = c.valid > wm * WTM, stored = false;
-    read_scales(c, 0, slot);
+    // Two stages.  After the barrier that publishes a step, the stage before
+    // it is refilled with the step after it: half of the copies go between the
+    // products that follow the barrier, half between the next slice's (later
+    // ones would land too late, all at once they block the waves).  The first
+    // fragments of a step are read before the last products of the one before.
+    // Copies are issued under no condition (past the last tile they copy
+    // zeros): the compiler would move the products behind the branch.
+    static_assert(STAGES == 2, "two stages");
+    XFrag xf[2][FM];
+    WFrag wf[2][FN];
+    constexpr int HALF = STEP_COPIES / 2, PRODUCTS = FM * FN;
+    auto copies = [&](int to, auto first_, auto m_) {  // those of the half from `first` on that follow product m
+      constexpr int FIRST = decltype(first_)::value, M = decltype(m_)::value;
+      constexpr int COUNT = FIRST ? STEP_COPIES - HALF : HALF;
+      constexpr int A = FIRST + COUNT * M / PRODUCTS, B = FIRST + COUNT * (M + 1) / PRODUCTS;
+      if constexpr (B > A) {
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<B - A>([&](auto q_) { issue_copy(to, std::integral_constant<int, A + decltype(q_)::value>{}); });
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, HALF>;
+    auto half_alone = [&](int to, auto first_) {
+      static_for<PRODUCTS>([&](auto m_) { copies(to, first_, m_); });
+    };
+    auto publish = [&]() {
+      wait_vmcnt<0>();
+      slot ^= 1;
+      hand_on(slot);
+      lds_barrier();
+    };
+    int t_next = 0;
+    Tile next = c;
+    issue_scales(0, 0);
+    half_alone(0, First{});
+    half_alone(0, Second{});
+    advance();
+    publish();
+    issue_scales(1, 0);
+    half_alone(1, First{});
     read_frags(0, 0, xf[0], wf[0]);
+    read_scales(c, 0, slot);
     while (true) {
       clear();
-      Tile next = c;
-      int t_next = 0;
 #pragma unroll 1
       for (int kt = 0; kt < steps; ++kt) {
-        if (alive) {
-          static_for<NS - 1>([&](auto s_) {
-            constexpr int S = decltype(s_)::value;
-            read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
-            multiply(xf[S & 1], wf[S & 1], s_);
-          });
-        }
-        const int old = st;
-        st = st + 1 == STAGES ? 0 : st + 1;
-        const bool last = kt + 1 == steps;
-        if (last) {
+        static_for<NS - 1>([&](auto s_) {
+          constexpr int S = decltype(s_)::value;
+          read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+          if constexpr (S == 0) {
+            multiply(xf[0], wf[0], s_, [&](auto m_) { copies(st ^ 1, Second{}, m_); });
+            advance();
+          } else {
+            multiply(xf[S & 1], wf[S & 1], s_, nothing);
+          }
+        });
+        publish();
+        st ^= 1;
+        if (kt + 2 == steps) {  // the next copies are the next tile's
           t_next = tile_at(++jc);
-          if (t_next >= 0) next = coord(t_next);
+          if (t_next >= 0) {
+            next = coord(t_next);
+            set_sources(next);
+          } else {
+            no_sources();  // what is still issued copies zeros
+          }
         }
-        const bool more = !last || t_next >= 0, alive_next = last ? next.valid > wm * WTM : alive;
-        if (more) {
-          // the next step is published, and every wave has read this one's
-          // stage: refill it; the next step's first fragments are read before
-          // this step's last products
-          publish(last ? 0 : kt + 1, stored);
-          stored = false;
-          feed(old);
-          if (alive_next) read_frags(st, 0, xf[0], wf[0]);
-        }
-        if (alive) multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{});
-        if (!last && alive) read_scales(c, kt + 1, slot);
+        issue_scales(kt + 2 < steps ? kt + 2 : kt + 2 - steps, 0);
+        read_frags(st, 0, xf[0], wf[0]);
+        multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{},
+                 [&](auto m_) { copies(st ^ 1, First{}, m_); });
+        read_scales(c, 0, slot);
       }
-      stored = epilogue(c);
+      epilogue(c);
       if (t_next < 0) break;
       c = next;
       steps = steps_of(c);
-      alive = c.valid > wm * WTM;
-      if (alive) read_scales(c, 0, slot);
     }
   }
   wait_vmcnt<0>();  // no copy in flight when the workgroup ends
