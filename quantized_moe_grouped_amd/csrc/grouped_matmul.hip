@@ -239,9 +239,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // 256-row FP4 tile 1000 of 5100 cycles.)
   constexpr int SPG = MX ? (KWAVES ? 512 : 1024) / BK : 1;  // k-steps of one group of scales
   constexpr int XW = (BM + 63) / 64, SROWS = MX ? XW * 64 + BN : 1;  // rows whose scales are staged
-  static_assert(!MX || SROWS <= NT, "a thread for each row's scales");
+  static_assert(!MX || (KWAVES ? SROWS <= NT : SROWS == NT), "a thread for each row's scales");
   constexpr int SB = BK / 128;  // words of a row's scales in one step
-  static_assert(!MX || KWAVES || (STAGES == 2 && (SB == 1 || SB == 2)), "scales are handed on a step ahead");
+  static_assert(!MX || KWAVES || SB == 1 || SB == 2, "words of a step");
 
   __shared__ __attribute__((aligned(16))) uint8_t sX[STAGES * X_BYTES];
   __shared__ __attribute__((aligned(16))) uint8_t sW[STAGES * W_BYTES];
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   };
   auto steps_of = [&](const Tile& c) -> int {
     const int s = (int)(((int64_t)c.r1 - c.r0 + BK - 1) / BK);
-    return KWAVES ? s : max(s, 2);  // at least two in the pipeline below, of zeros if need be
+    return KWAVES ? s : max(s, STAGES);  // the pipeline below wants that many, of zeros if need be
   };
 
   // column of the weights for column q of the tile; -1 past the last
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   uint32_t x_size = 0, w_size = 0, xs_size = 0, ws_size = 0;
   int r_left = 0;                  // of the reduction, from the step on
   uint32_t x_skip = 0, w_skip = 0; // rows across the reduction: bytes of a row before the tile
-  uint32_t x_off[XI], w_off[WI], s_off = kOutside, s_odd = 0;
+  uint32_t x_off[XI], w_off[WI], s_off[2] = {kOutside, kOutside}, s_odd[2] = {0, 0};
   const int x_ch = XCOL ? 0 : ((lane % XC) ^ swz_row<XC>(tid / XC)) * 16;
   const int w_ch = WCOL ? 0 : ((lane % WC) ^ swz_row<WC>(tid / WC)) * 16;
   auto cut = [](int64_t bytes) -> uint32_t { return (uint32_t)(bytes > (int64_t)kOutside ? (int64_t)kOutside : bytes); };
@@ -385,6 +385,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         w_off[q] = col >= 0 ? (uint32_t)(col - c.n0) * (uint32_t)w_row + w_ch : kOutside;
       }
     }
+  };
+  auto set_scale_sources = [&](const Tile& c) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
     if constexpr (MX) {
       const uint8_t* xb = p.xs + c.m0 * s_row;
       const uint8_t* wb = p.ws + ((int64_t)c.g * p.n + c.n0) * s_row;
@@ -396,11 +400,14 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       xs_size = cut((p.xs + p.m * s_row - xs_at + 3) & ~(int64_t)3);
       ws_size = cut((p.ws + (int64_t)p.e * p.n * s_row - ws_at + 3) & ~(int64_t)3);
       // of the staged rows: x first, then columns
-      const uint32_t from = tid < XW * 64 ? xf : wf;
-      const int row = tid < XW * 64 ? (tid < c.valid ? tid : -1) : (tid < SROWS ? column(c, tid - XW * 64) : -1);
-      const uint32_t at = (uint32_t)(tid < XW * 64 ? row : row - c.n0) * (uint32_t)s_row + from;
-      s_off = row >= 0 ? at & ~3u : kOutside;
-      s_odd = (at & 3) * 8;  // bits
+#pragma unroll
+      for (int u = 0; u < (KWAVES ? 1 : 2); ++u) {
+        const int i = KWAVES ? tid : (tid & ~63) + u * 32 + ((tid & 63) >> 1);
+        const int row = i < XW * 64 ? (i < c.valid ? i : -1) : (i < SROWS ? column(c, i - XW * 64) : -1);
+        const uint32_t at = (uint32_t)(i < XW * 64 ? row : row - c.n0) * (uint32_t)s_row + (i < XW * 64 ? xf : wf);
+        s_off[u] = row >= 0 ? at & ~3u : kOutside;
+        s_odd[u] = (at & 3) * 8;  // bits
+      }
     }
   };
   // Copies of the stream's next step (step kt of its tile) into stage `st`:
@@ -408,50 +415,71 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // one copy after the other.  A copy keeps the CU's address path busy for 16
   // to 21 cycles; all at once they block every wave in turn, so they are
   // issued between the products.
-  typedef uint32_t v8u __attribute__((ext_vector_type(8)));
-  v8u sc_group;           // this thread's row: what is left of its group of scales, the next step's first
-  uint32_t sc_last = 0, sc_odd = 0;
-  int sc_blocks = 0;      // blocks of the step that exist
+  // Without KWAVES two lanes take a row's 32 bytes, 16 each (a fetch of 64
+  // separate lines would hold the address path four times as long): lane l of
+  // copy u the half l & 1 of staged row 64 wave + 32 u + l / 2.
+  v4u sc_half[2];
+  uint32_t sc_next[2] = {0, 0}, sc_odd[2] = {0, 0};  // the dword after the second half; bits to shift by
   auto issue_scales = [&](int kt, int slot) {
-    if constexpr (MX) {
-      sc_blocks = min(BK, r_left) / 32;
-      if (kt % SPG == 0 && (SROWS == NT || wave * 64 < SROWS)) {
+    if constexpr (MX && KWAVES) {
+      if (kt % SPG == 0 && wave * 64 < SROWS) {
         const v4i r = wave < XW ? buffer(xs_at, xs_size) : buffer(ws_at, ws_size);
-        if constexpr (KWAVES) {
-          const uint32_t at = kt / SPG * 16;
-          copy16(r, s_off + at, __builtin_amdgcn_readfirstlane(lds_addr(s_sc)) + (slot * SROWS + wave * 64) * 16);
-          if (s_split)
-            copy4(r, s_off + at + 16, __builtin_amdgcn_readfirstlane(lds_addr(s_sc2)) + (slot * SROWS + wave * 64) * 4);
-        } else {
-          const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
-              (void*)(((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x), 0, r.z, 0x00020000);
-          const int at = (int)s_off + kt / SPG * 32;
-          const v4u lo = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
-          const v4u hi = __builtin_amdgcn_raw_buffer_load_b128(b, at + 16, 0, 0);
-          sc_group = v8u{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-          sc_last = __builtin_amdgcn_raw_buffer_load_b32(b, at + 32, 0, 0);
-          sc_odd = s_odd;
+        const uint32_t at = kt / SPG * 16;
+        copy16(r, s_off[0] + at, __builtin_amdgcn_readfirstlane(lds_addr(s_sc)) + (slot * SROWS + wave * 64) * 16);
+        if (s_split)
+          copy4(r, s_off[0] + at + 16, __builtin_amdgcn_readfirstlane(lds_addr(s_sc2)) + (slot * SROWS + wave * 64) * 4);
+      }
+    } else if constexpr (MX) {
+      if (kt % SPG == 0) {
+        const v4i r = wave < XW ? buffer(xs_at, xs_size) : buffer(ws_at, ws_size);
+        const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x), 0, r.z, 0x00020000);
+        const int at = kt / SPG * 32 + (lane & 1) * 16;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          sc_half[u] = __builtin_amdgcn_raw_buffer_load_b128(b, (int)s_off[u] + at, 0, 0);
+          if (s_split) sc_next[u] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)s_off[u] + at + 16, 0, 0);
+          sc_odd[u] = s_odd[u];
         }
       }
     }
   };
-  // The coming step's scales, from the thread that holds its row's; blocks
-  // past k become zero bytes (2^-127, where the next row's may be a NaN).
-  auto hand_on = [&](int slot) {
+  // The coming step's scales, from the lanes that hold them; blocks past k
+  // become zero bytes (2^-127, where the next row's may be a NaN).
+  auto hand_on = [&](int kt, int slot) {
     if constexpr (MX && !KWAVES) {
-      if (SROWS == NT || wave * 64 < SROWS) {
+      constexpr int PER = SPG / 2;  // steps of a half
+      const int pos = kt % SPG, w = pos % PER * SB;
+      const bool mine = (lane & 1) == pos / PER;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const v4u v = sc_half[u];
         uint32_t d[SB];
+        if constexpr (SB == 2) {
+          d[0] = w ? v.z : v.x;
+          d[1] = w ? v.w : v.y;
+        } else {
+          d[0] = w & 2 ? (w & 1 ? v.w : v.z) : (w & 1 ? v.y : v.x);
+        }
+        if (s_split) {
+          uint32_t next = w + SB == 4 ? sc_next[u] : (SB == 2 ? v.z : (w == 0 ? v.y : w == 1 ? v.z : v.w));
+          if constexpr (SB == 2) {
+            d[0] = __builtin_amdgcn_alignbit(d[1], d[0], sc_odd[u]);
+            d[1] = __builtin_amdgcn_alignbit(next, d[1], sc_odd[u]);
+          } else {
+            d[0] = __builtin_amdgcn_alignbit(next, d[0], sc_odd[u]);
+          }
+        }
 #pragma unroll
         for (int q = 0; q < SB; ++q) {
-          d[q] = __builtin_amdgcn_alignbit(sc_group[q + 1], sc_group[q], sc_odd);
-          const int bytes = sc_blocks - 4 * q;
+          const int bytes = ((int)p.k - kt * BK) / 32 - 4 * q;
           if (bytes < 4) d[q] &= bytes <= 0 ? 0u : (1u << (8 * bytes)) - 1;
         }
-        uint32_t* to = &s_step[(slot * SROWS + tid) * SB];
-        if constexpr (SB == 2) *(uint64_t*)to = (uint64_t)d[1] << 32 | d[0];
-        else *to = d[0];
-        if constexpr (SB == 2) sc_group = v8u{sc_group[2], sc_group[3], sc_group[4], sc_group[5], sc_group[6], sc_group[7], sc_last, 0};
-        else sc_group = v8u{sc_group[1], sc_group[2], sc_group[3], sc_group[4], sc_group[5], sc_group[6], sc_group[7], sc_last};
+        uint32_t* to = &s_step[(slot * SROWS + wave * 64 + u * 32 + (lane >> 1)) * SB];
+        if (mine) {
+          if constexpr (SB == 2) *(uint64_t*)to = (uint64_t)d[1] << 32 | d[0];
+          else *to = d[0];
+        }
       }
     }
   };
@@ -481,9 +509,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     r_left = max(r_left - BK, 0);
   };
   auto no_sources = [&]() {
-    x_size = w_size = xs_size = ws_size = 0;
+    x_size = w_size = 0;
     r_left = 0;
   };
+  auto no_scale_sources = [&]() { xs_size = ws_size = 0; };
 
   // ---- fragments.  A fragment holds 32 rows (x) or columns (w) of one slice:
   // lane l row l % 32, and its h = l / 32 half of the slice.  The addresses of
@@ -581,20 +610,33 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       for (int i = 0; i < FM; ++i) xsc[i] = one(i * 32 + (lane & 31), s_split ? ((c.m0 + lane) & 1) * 2 : 0);
 #pragma unroll
       for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + j * 32 + (lane & 31), s_split ? (lane & 1) * 2 : 0);
-    } else if constexpr (MX) {
-      auto one = [&](int row) -> uint32_t {
-        const uint32_t* words = &s_step[(slot * SROWS + row) * SB];
-        if constexpr (SB == 2) {
-          const uint64_t two = *(const uint64_t*)words;
-          return __builtin_amdgcn_perm((uint32_t)(two >> 32), (uint32_t)two, h ? 0x07050301u : 0x06040200u);
-        } else {
-          return *words >> (8 * h);
-        }
+    }
+  };
+  // Without KWAVES in two halves, with products between: the words of the
+  // coming step, and what the lane keeps of them.
+  using Words = std::conditional_t<SB == 2, uint64_t, uint32_t>;
+  Words x_words[FM], w_words[FN];
+  auto fetch_scales = [&](int slot) {
+    if constexpr (MX && !KWAVES) {
+      const Words* base = (const Words*)s_step + slot * SROWS;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) x_words[i] = base[wm * WTM + i * 32 + (lane & 31)];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) w_words[j] = base[XW * 64 + wn * WTN + j * 32 + (lane & 31)];
+    }
+  };
+  auto keep_scales = [&]() {
+    if constexpr (MX && !KWAVES) {
+      auto one = [&](Words v) -> uint32_t {
+        if constexpr (SB == 2)
+          return __builtin_amdgcn_perm((uint32_t)(v >> 32), (uint32_t)v, h ? 0x07050301u : 0x06040200u);
+        else
+          return v >> (8 * h);
       };
 #pragma unroll
-      for (int i = 0; i < FM; ++i) xsc[i] = one(wm * WTM + i * 32 + (lane & 31));
+      for (int i = 0; i < FM; ++i) xsc[i] = one(x_words[i]);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) wsc[j] = one(XW * 64 + wn * WTN + j * 32 + (lane & 31));
+      for (int j = 0; j < FN; ++j) wsc[j] = one(w_words[j]);
     }
   };
 
@@ -712,9 +754,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   int steps = steps_of(c), jc = 0;
   int st = 0, slot = KWAVES ? STAGES - 1 : 0;  // computing: stage, slot of the scales in use
   set_sources(c);
+  set_scale_sources(c);
   // A step of the computing stream has landed (its copies and all before
   // them): publish it.
-  constexpr int YOUNGER = (STAGES - 2) * STEP_COPIES;
+  constexpr int YOUNGER = (STAGES - 2) * STEP_COPIES;  // copies that may be in flight then
 
   if constexpr (KWAVES) {
     // A stream of copies STAGES - 1 steps ahead that crosses the tiles' borders
@@ -735,8 +778,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           const Tile lc = coord(t);
           lsteps = steps_of(lc);
           set_sources(lc);
+          set_scale_sources(lc);
         } else {
           no_sources();  // what is still issued copies zeros
+          no_scale_sources();
         }
       }
     };
@@ -792,17 +837,18 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       // s_sum is written again only after the next tile's first barrier
     }
   } else {
-    // Two stages.  After the barrier that publishes a step, the stage before
-    // it is refilled with the step after it: half of the copies go between the
-    // products that follow the barrier, half between the next slice's (later
-    // ones would land too late, all at once they block the waves).  The first
-    // fragments of a step are read before the last products of the one before.
-    // Copies are issued under no condition (past the last tile they copy
-    // zeros): the compiler would move the products behind the branch.
-    static_assert(STAGES == 2, "two stages");
+    // After the barrier that publishes a step, the stage before it is refilled
+    // with the step STAGES - 1 after it.  With four slices to a step half of
+    // the copies go between the products that follow the barrier and half
+    // between the next slice's, with two slices all between the former (all at
+    // once they block the waves; later ones land too late: a quarter later
+    // cost 2-4%).  The first fragments of a step are read before the last
+    // products of the one before.  Copies are issued under no condition (past
+    // the last tile they copy zeros): the compiler would move the products
+    // behind the branch.
     XFrag xf[2][FM];
     WFrag wf[2][FN];
-    constexpr int HALF = STEP_COPIES / 2, PRODUCTS = FM * FN;
+    constexpr int HALF = NS == 2 ? STEP_COPIES : STEP_COPIES / 2, PRODUCTS = FM * FN;
     auto copies = [&](int to, auto first_, auto m_) {  // those of the half from `first` on that follow product m
       constexpr int FIRST = decltype(first_)::value, M = decltype(m_)::value;
       constexpr int COUNT = FIRST ? STEP_COPIES - HALF : HALF;
@@ -815,26 +861,28 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     };
     using First = std::integral_constant<int, 0>;
     using Second = std::integral_constant<int, HALF>;
-    auto half_alone = [&](int to, auto first_) {
-      static_for<PRODUCTS>([&](auto m_) { copies(to, first_, m_); });
+    auto all_copies = [&](int to) {
+      static_for<STEP_COPIES>([&](auto q_) { issue_copy(to, q_); });
+      advance();
     };
-    auto publish = [&]() {
-      wait_vmcnt<0>();
+    auto publish = [&](int nk) {  // step nk of a tile
+      wait_vmcnt<YOUNGER>();
       slot ^= 1;
-      hand_on(slot);
+      hand_on(nk, slot);
       lds_barrier();
     };
-    int t_next = 0;
+    int t_next = 0, refill = STAGES - 1;
     Tile next = c;
     issue_scales(0, 0);
-    half_alone(0, First{});
-    half_alone(0, Second{});
-    advance();
-    publish();
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) all_copies(s);
+    publish(0);
     issue_scales(1, 0);
-    half_alone(1, First{});
+    static_for<HALF>([&](auto q_) { issue_copy(STAGES - 1, q_); });
+    if constexpr (HALF == STEP_COPIES) advance();
+    fetch_scales(slot);
     read_frags(0, 0, xf[0], wf[0]);
-    read_scales(c, 0, slot);
+    keep_scales();
     while (true) {
       clear();
 #pragma unroll 1
@@ -842,16 +890,17 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         static_for<NS - 1>([&](auto s_) {
           constexpr int S = decltype(s_)::value;
           read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
-          if constexpr (S == 0) {
-            multiply(xf[0], wf[0], s_, [&](auto m_) { copies(st ^ 1, Second{}, m_); });
+          if constexpr (S == 0 && HALF < STEP_COPIES) {
+            multiply(xf[0], wf[0], s_, [&](auto m_) { copies(refill, Second{}, m_); });
             advance();
           } else {
             multiply(xf[S & 1], wf[S & 1], s_, nothing);
           }
         });
-        publish();
-        st ^= 1;
-        if (kt + 2 == steps) {  // the next copies are the next tile's
+        publish(kt + 1 < steps ? kt + 1 : 0);
+        refill = st;
+        st = st + 1 == STAGES ? 0 : st + 1;
+        if (kt + STAGES == steps) {  // the next copies are the next tile's
           t_next = tile_at(++jc);
           if (t_next >= 0) {
             next = coord(t_next);
@@ -860,11 +909,19 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
             no_sources();  // what is still issued copies zeros
           }
         }
-        issue_scales(kt + 2 < steps ? kt + 2 : kt + 2 - steps, 0);
+        if constexpr (MX) {  // scales are two steps ahead whatever the stages
+          if (kt + 2 == steps) {
+            if (t_next >= 0) set_scale_sources(next);
+            else no_scale_sources();
+          }
+          issue_scales(kt + 2 < steps ? kt + 2 : kt + 2 - steps, 0);
+        }
+        fetch_scales(slot);
         read_frags(st, 0, xf[0], wf[0]);
         multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{},
-                 [&](auto m_) { copies(st ^ 1, First{}, m_); });
-        read_scales(c, 0, slot);
+                 [&](auto m_) { copies(refill, First{}, m_); });
+        if constexpr (HALF == STEP_COPIES) advance();
+        keep_scales();
       }
       epilogue(c);
       if (t_next < 0) break;
@@ -919,6 +976,15 @@ int tuning(const int64_t* t, int64_t len, int64_t* rows, int64_t* height, int64_
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// 256-row tiles or 128-row ones, of which `large` and `middle` (in halves) lie
+// along M: by the rounds of the chip that they make, a round of 512 small
+// tiles (two a CU) taking 0.6 of a round of 256 large ones (measured at 32768 x
+// 2048 x 7168 over 32 experts: 1.15 against 0.95 ms for the same work).
+Kind larger_kind(int64_t large, int64_t middle, int64_t columns) {
+  const int64_t l = ceil_div(large * ceil_div(columns, 256), 2 * 256), m = ceil_div(middle * ceil_div(columns, 128), 2 * 512);
+  return l * 10 <= m * 6 ? kLarge : kMiddle;
+}
 
 int grid_of(const Plan& pl, int64_t tiles, int64_t cap) {
   int64_t g = 256 * kPerCu[pl.kind];
@@ -984,15 +1050,18 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : xt == GMMFR_DT_FLOAT16 ? kF16 : per == 2 ? kFp4 : kFp8;
   pl->glu = glu;
   pl->col = a->transpose_w == 0;
-  // rows an expert is likely to have: experts without rows cost nothing
-  const int64_t avg = rows > 0 ? rows : m / (e < m ? e : (m > 0 ? m : 1));
+  // Rows an expert is likely to have (experts without rows cost nothing), and
+  // half a tile of each expert's cut short.  Up to 32 rows the narrow tiles
+  // that stream the weights (256 experts of 8 rows on average: 0.52 against
+  // 0.55 ms with 128-row tiles; 32 of 128: 0.45 against 0.27).
+  const int64_t parts = e < m ? e : m, avg = rows > 0 ? rows : m / (parts > 0 ? parts : 1);
   pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
-                    : (avg >= 192 ? kLarge : avg > 32 ? kMiddle : kSmall);
+                    : (avg <= 32 ? kSmall : larger_kind(2 * m / 256 + parts, 2 * m / 128 + parts, n));
   const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
   p.tiles_m = 0;
   p.tiles_n = (int32_t)ceil_div(glu ? n / 2 : n, tn);
   // at most this many tiles: whole ones, and one part a non-empty expert
-  const int64_t tiles = (m / kTileM[pl->kind] + (e < m ? e : m)) * p.tiles_n;
+  const int64_t tiles = (m / kTileM[pl->kind] + parts) * p.tiles_n;
   if (tiles >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
   pl->grid = grid_of(*pl, tiles, cap);
   return GMMFR_OK;
@@ -1032,8 +1101,8 @@ int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : kF16;
   pl->glu = false;
   pl->col = true;
-  const int64_t large = e * ceil_div(k, 256) * ceil_div(n, 256);
-  pl->kind = height ? (height == 256 ? kLarge : kMiddle) : (large >= 512 ? kLarge : kMiddle);
+  pl->kind = height ? (height == 256 ? kLarge : kMiddle)
+                    : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n);
   p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);
   p.tiles_n = (int32_t)ceil_div(n, kTileN[pl->kind]);
   pl->grid = grid_of(*pl, e * p.tiles_m * p.tiles_n, cap);
@@ -1046,8 +1115,13 @@ void launch(const Plan& pl, hipStream_t s) {
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
   constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
   if (pl.kind == kLarge)
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, BK, 4, 2, 2, false, 2>), dim3(pl.grid),
-                       dim3(512), dyn, s, pl.p);
+    // the weight gradient's stages are whole rows of a tile whatever their
+    // length: four short ones hide more of a copy's way than two long ones
+    // (1.27 -> 1.20 ms at 32768 x 2048 x 7168); with rows along the reduction
+    // short stages would take half a line at a time (2-7% slower)
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK, 4, 2, WGRAD ? 4 : 2,
+                                       false, 2>),
+                       dim3(pl.grid), dim3(512), dyn, s, pl.p);
   else if (pl.kind == kMiddle)
     hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>), dim3(pl.grid),
                        dim3(256), dyn, s, pl.p);
