@@ -122,14 +122,14 @@ def lib():
         L.gmm_quant_permute_profiled.argtypes = [ctypes.POINTER(QpArgs), ctypes.c_void_p, ctypes.c_size_t,
                                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
         L.gmm_quant_permute_profiled.restype = ctypes.c_int
+        # arguments of these as void*: a struct by reference, or its bytes
         for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad"):
-            args = ctypes.POINTER(GwArgs if name.endswith("wgrad") else GmArgs)
-            getattr(L, name + "_workspace").argtypes = [args, ctypes.POINTER(ctypes.c_size_t)]
+            getattr(L, name + "_workspace").argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]
             getattr(L, name + "_workspace").restype = ctypes.c_int
-            getattr(L, name).argtypes = [args, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+            getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
         for name in ("gmm_mx_quantize", "gmm_mx_dequantize"):
-            getattr(L, name).argtypes = [ctypes.POINTER(MqArgs), ctypes.c_void_p]
+            getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
         L.gmmfr_status_string.argtypes = [ctypes.c_int]
         L.gmmfr_status_string.restype = ctypes.c_char_p
@@ -394,6 +394,8 @@ def _quant_permute_on(hidden, expert_ids, num_experts, topk_weights, expert_offs
 # ------------------------------------------------- grouped products and MX quantisation
 
 _pack_tensor = struct.Struct("=Qii4q").pack
+_pack_qii = struct.Struct("=qii").pack
+_pack_ii = struct.Struct("=ii").pack
 _ABSENT = _pack_tensor(0, 0, 0, 0, 0, 0, 0)
 _PAD = {n: (0,) * (4 - n) for n in range(5)}
 _codes_of: dict = {}
@@ -425,13 +427,26 @@ def _packed_tuning(tuning_config):
     return tuning, struct.pack("=Qq", ctypes.addressof(tuning), len(tuning_config))
 
 
+def _gm_bytes(x, w, group_list, y, x_scale, w_scale, group_list_type, transpose_w, activation, tail) -> bytes:
+    return b"".join((_packed(x), _packed(w), _packed(x_scale), _packed(w_scale), _packed(group_list), _packed(y),
+                     _pack_qii(group_list_type, bool(transpose_w), ACTIVATION[activation]), tail))
+
+
+def _gw_bytes(x, dy, group_list, dw, group_list_type, accumulate, tail) -> bytes:
+    return b"".join((_packed(x), _packed(dy), _packed(group_list), _packed(dw),
+                     _pack_qii(group_list_type, bool(accumulate), 0), tail))
+
+
+def _mq_bytes(x, codes, scales, transpose) -> bytes:
+    return b"".join((_packed(x), _packed(codes), _packed(scales), _pack_ii(bool(transpose), 0)))
+
+
 def make_gm_args(x, w, group_list, y, *, x_scale=None, w_scale=None, group_list_type: int = 0,
                  transpose_w: bool = False, activation: Optional[str] = None,
                  tuning_config: Optional[Sequence[int]] = None):
     """C arguments of gmm_grouped_matmul.  Returns (args, keepalive), as make_args."""
     tuning, tail = _packed_tuning(tuning_config)
-    raw = b"".join((_packed(x), _packed(w), _packed(x_scale), _packed(w_scale), _packed(group_list), _packed(y),
-                    struct.pack("=qii", group_list_type, bool(transpose_w), ACTIVATION[activation]), tail))
+    raw = _gm_bytes(x, w, group_list, y, x_scale, w_scale, group_list_type, transpose_w, activation, tail)
     return GmArgs.from_buffer_copy(raw), (x, w, group_list, y, x_scale, w_scale, tuning)
 
 
@@ -439,15 +454,13 @@ def make_gw_args(x, dy, group_list, dw, *, group_list_type: int = 0, accumulate:
                  tuning_config: Optional[Sequence[int]] = None):
     """C arguments of gmm_grouped_matmul_wgrad.  Returns (args, keepalive)."""
     tuning, tail = _packed_tuning(tuning_config)
-    raw = b"".join((_packed(x), _packed(dy), _packed(group_list), _packed(dw),
-                    struct.pack("=qii", group_list_type, bool(accumulate), 0), tail))
+    raw = _gw_bytes(x, dy, group_list, dw, group_list_type, accumulate, tail)
     return GwArgs.from_buffer_copy(raw), (x, dy, group_list, dw, tuning)
 
 
 def make_mq_args(x, codes, scales, *, transpose: bool = False):
     """C arguments of gmm_mx_quantize and gmm_mx_dequantize.  Returns (args, keepalive)."""
-    raw = b"".join((_packed(x), _packed(codes), _packed(scales), struct.pack("=ii", bool(transpose), 0)))
-    return MqArgs.from_buffer_copy(raw), (x, codes, scales)
+    return MqArgs.from_buffer_copy(_mq_bytes(x, codes, scales, transpose)), (x, codes, scales)
 
 
 def _check_device(dev, *tensors) -> None:
@@ -459,32 +472,32 @@ def _check_device(dev, *tensors) -> None:
             raise ValueError(f"tensors must be on one device: {t.device} and {dev}")
 
 
-def _on(dev, stream, call):
-    """call(raw stream handle) with `dev` current and, where a stream is given,
-    that stream too (so that what the call allocates comes from its pool)."""
+def _on(dev, stream, call, *args):
+    """call(raw stream handle, *args) with `dev` current and, where a stream is
+    given, that stream too (so that what the call allocates comes from its pool)."""
     import torch
     if stream is None and torch.cuda.current_device() == dev.index:
-        return call(torch.cuda.current_stream(dev).cuda_stream)
+        return call(torch._C._cuda_getCurrentRawStream(dev.index), *args)
     with torch.cuda.device(dev):
         ts = _torch_stream(stream)
         if ts.device != dev:
             raise ValueError(f"the stream is on {ts.device}, the tensors on {dev}")
         with torch.cuda.stream(ts):
-            return call(ts.cuda_stream)
+            return call(ts.cuda_stream, *args)
 
 
-def _two_stage(name: str, args, workspace, dev, handle) -> None:
-    """Size the workspace, allocate it if none is given, enqueue."""
-    import torch
+def _enqueue(name: str, raw: bytes, workspace, dev, handle) -> None:
+    """Stage 2; where it wants a workspace and none is given, stage 1 sizes one first."""
     L = lib()
-    need = ctypes.c_size_t(0)
-    st = getattr(L, name + "_workspace")(args, need)
-    if st != OK:
-        raise GmmfrError(st, name + "_workspace")
-    if workspace is None and need.value:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
     ptr, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = getattr(L, name)(args, ptr, size, handle)
+    st = getattr(L, name)(raw, ptr, size, handle)
+    if st == ERR_WORKSPACE and workspace is None:
+        import torch
+        need = ctypes.c_size_t(0)
+        st = getattr(L, name + "_workspace")(raw, need)
+        if st == OK:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+            st = getattr(L, name)(raw, workspace.data_ptr(), need.value, handle)
     if st != OK:
         raise GmmfrError(st, name)
 
@@ -500,23 +513,23 @@ def grouped_matmul(x, w, group_list, *, x_scale=None, w_scale=None, out=None, ou
     their scales.  Returns out, allocated as (m, n or n/2) if none is given, in
     out_dtype (default: x's type; bf16 for microscaled x); rows behind the last
     group are left as they are."""
-    import torch
-    dev = x.device
-    _check_device(dev, w, group_list, x_scale, w_scale, out, workspace)
+    _check_device(x.device, w, group_list, x_scale, w_scale, out, workspace)
+    return _on(x.device, stream, _grouped_matmul, x, w, group_list, x_scale, w_scale, out, out_dtype, group_list_type,
+               transpose_w, activation, tuning_config, workspace)
 
-    def call(handle):
-        y = out
-        if y is None:
-            columns = w.shape[1 if transpose_w else 2] // (2 if ACTIVATION[activation] else 1)
-            dtype = out_dtype or (x.dtype if x.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16)
-            y = torch.empty((x.shape[0], columns), dtype=dtype, device=dev)
-        args, keep = make_gm_args(x, w, group_list, y, x_scale=x_scale, w_scale=w_scale,
-                                  group_list_type=group_list_type, transpose_w=transpose_w, activation=activation,
-                                  tuning_config=tuning_config)
-        _two_stage("gmm_grouped_matmul", args, workspace, dev, handle)
-        del keep
-        return y
-    return _on(dev, stream, call)
+
+def _grouped_matmul(handle, x, w, group_list, x_scale, w_scale, out, out_dtype, group_list_type, transpose_w,
+                    activation, tuning_config, workspace):
+    import torch
+    if out is None:
+        columns = w.shape[1 if transpose_w else 2] // (2 if ACTIVATION[activation] else 1)
+        dtype = out_dtype or (x.dtype if x.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16)
+        out = torch.empty((x.shape[0], columns), dtype=dtype, device=x.device)
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gm_bytes(x, w, group_list, out, x_scale, w_scale, group_list_type, transpose_w, activation, tail)
+    _enqueue("gmm_grouped_matmul", raw, workspace, x.device, handle)
+    del tuning  # the host array lives until the call has read it
+    return out
 
 
 def grouped_matmul_wgrad(x, dy, group_list, *, out=None, out_dtype=None, accumulate: bool = False,
@@ -525,66 +538,66 @@ def grouped_matmul_wgrad(x, dy, group_list, *, out=None, out_dtype=None, accumul
     """Gradient of a grouped product's weights (e,k,n): x_g^T dy_g for every
     expert, in out_dtype (default fp32), zeros for one without rows.
     accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x)."""
-    import torch
-    dev = x.device
-    _check_device(dev, dy, group_list, out, workspace)
+    _check_device(x.device, dy, group_list, out, workspace)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
+    return _on(x.device, stream, _grouped_matmul_wgrad, x, dy, group_list, out, out_dtype, accumulate,
+               group_list_type, tuning_config, workspace)
 
-    def call(handle):
-        dw = out
-        if dw is None:
-            dw = torch.empty((group_list.shape[0], x.shape[1], dy.shape[1]), dtype=out_dtype or torch.float32, device=dev)
-        args, keep = make_gw_args(x, dy, group_list, dw, group_list_type=group_list_type, accumulate=accumulate,
-                                  tuning_config=tuning_config)
-        _two_stage("gmm_grouped_matmul_wgrad", args, workspace, dev, handle)
-        del keep
-        return dw
-    return _on(dev, stream, call)
+
+def _grouped_matmul_wgrad(handle, x, dy, group_list, out, out_dtype, accumulate, group_list_type, tuning_config,
+                          workspace):
+    import torch
+    if out is None:
+        out = torch.empty((group_list.shape[0], x.shape[1], dy.shape[1]), dtype=out_dtype or torch.float32,
+                          device=x.device)
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gw_bytes(x, dy, group_list, out, group_list_type, accumulate, tail)
+    _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, x.device, handle)
+    del tuning
+    return out
 
 
 def mx_quantize(x, *, format: str = "fp4", transpose: bool = False, stream=None):
     """(codes, scales) of x (rows,k) or (e,n,k), or with transpose of weights
     (e,k,n), which become (e,n,k): FP4 (k/2 bytes a row) or FP8 codes with one
     E8M0 scale per 32 values, (..., k/64, 2)."""
-    import torch
-    dev = x.device
-    _check_device(dev)
     if format not in ("fp4", "fp8"):
         raise ValueError(f"unknown format {format!r}")
     if transpose and x.dim() != 3:
         raise ValueError("transpose takes weights (e,k,n)")
+    _check_device(x.device)
+    return _on(x.device, stream, _mx_quantize, x, format, transpose)
 
-    def call(handle):
-        lead, k = ((x.shape[0], x.shape[2]), x.shape[1]) if transpose else (tuple(x.shape[:-1]), x.shape[-1])
-        if format == "fp4":
-            codes = torch.empty((*lead, k // 2), dtype=torch.float4_e2m1fn_x2, device=dev)
-        else:
-            codes = torch.empty((*lead, k), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((*lead, k // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
-        args, keep = make_mq_args(x, codes, scales, transpose=transpose)
-        st = lib().gmm_mx_quantize(args, handle)
-        if st != OK:
-            raise GmmfrError(st, "gmm_mx_quantize")
-        del keep
-        return codes, scales
-    return _on(dev, stream, call)
+
+def _mx_quantize(handle, x, format, transpose):
+    import torch
+    shape = x.shape
+    lead, k = ((shape[0], shape[2]), shape[1]) if transpose else (shape[:-1], shape[-1])
+    if format == "fp4":
+        codes = torch.empty((*lead, k // 2), dtype=torch.float4_e2m1fn_x2, device=x.device)
+    else:
+        codes = torch.empty((*lead, k), dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty((*lead, k // 64, 2), dtype=torch.float8_e8m0fnu, device=x.device)
+    st = lib().gmm_mx_quantize(_mq_bytes(x, codes, scales, transpose), handle)
+    if st != OK:
+        raise GmmfrError(st, "gmm_mx_quantize")
+    return codes, scales
 
 
 def mx_dequantize(codes, scales, *, dtype=None, stream=None):
     """The values that codes and scales stand for, (rows,k) or (e,n,k), in
     dtype (bf16 by default, fp16 or fp32)."""
-    import torch
-    dev = codes.device
-    _check_device(dev, scales)
+    _check_device(codes.device, scales)
+    return _on(codes.device, stream, _mx_dequantize, codes, scales, dtype)
 
-    def call(handle):
-        per = 2 if codes.dtype == torch.float4_e2m1fn_x2 else 1
-        x = torch.empty((*codes.shape[:-1], codes.shape[-1] * per), dtype=dtype or torch.bfloat16, device=dev)
-        args, keep = make_mq_args(x, codes, scales)
-        st = lib().gmm_mx_dequantize(args, handle)
-        if st != OK:
-            raise GmmfrError(st, "gmm_mx_dequantize")
-        del keep
-        return x
-    return _on(dev, stream, call)
+
+def _mx_dequantize(handle, codes, scales, dtype):
+    import torch
+    shape = codes.shape
+    per = 2 if codes.dtype == torch.float4_e2m1fn_x2 else 1
+    x = torch.empty((*shape[:-1], shape[-1] * per), dtype=dtype or torch.bfloat16, device=codes.device)
+    st = lib().gmm_mx_dequantize(_mq_bytes(x, codes, scales, False), handle)
+    if st != OK:
+        raise GmmfrError(st, "gmm_mx_dequantize")
+    return x
