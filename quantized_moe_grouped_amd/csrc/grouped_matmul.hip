@@ -640,7 +640,19 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     }
   };
 
+  // 256 accumulators a lane (one wave a SIMD) live in the accumulation
+  // registers, and are read from there one by one when they are stored
+  constexpr bool IN_AGPRS = FM * FN == 16;
   v16f acc[FM][FN];
+  auto sum_at = [&](int i, int j, int r) -> float {
+    if constexpr (IN_AGPRS) {
+      float o;
+      asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(o) : "a"(acc[i][j][r]));
+      return o;
+    } else {
+      return acc[i][j][r];
+    }
+  };
   // between(m): what is issued after product m of the slice
   auto multiply = [&](XFrag (&xf)[FM], WFrag (&wf)[FN], auto s_, auto between) {
     constexpr int S = KWAVES ? 0 : decltype(s_)::value * (NS == 4 ? 1 : 2);  // byte of the scale registers
@@ -662,7 +674,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     // with the fragments of all its slices held until then.
     static_for<FM * FN>([&](auto m_) {
       v16f& a = acc[decltype(m_)::value / FN][decltype(m_)::value % FN];
-      asm volatile("" : "+v"(a));
+      if constexpr (IN_AGPRS) asm volatile("" : "+a"(a));
+      else asm volatile("" : "+v"(a));
     });
   };
   auto nothing = [](auto) {};
@@ -714,6 +727,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   auto epilogue = [&](const Tile& c) -> bool {
     int lane = threadIdx.x & 63;  // opaque, as in set_sources
     asm volatile("" : "+v"(lane));
+    // sum_at's asm reads products' results: past the 18 wait states that the
+    // last of them may need
+    if constexpr (IN_AGPRS) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if constexpr (GLU) {
@@ -724,8 +740,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           for (int r = 0; r < 16; ++r) {
             // u / (1 + 2^(-u log2 e)) * v with the hardware's 2^x and 1/x, each
             // within 1 ulp; the rounded exponent adds |u| 2^-24
-            const float u = acc[i][j][r];
-            v[r] = u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f)) * acc[i][j + 1][r];
+            const float u = sum_at(i, j, r);
+            v[r] = u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f)) * sum_at(i, j + 1, r);
           }
           store_block(c, lane, i, (wn * WTN + j * 32) / 2, v);
         }
@@ -734,7 +750,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         for (int j = 0; j < FN; ++j) {
           float v[16];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+          for (int r = 0; r < 16; ++r) v[r] = sum_at(i, j, r);
           store_block(c, lane, i, wn * WTN + j * 32, v);
         }
       }
@@ -838,20 +854,20 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     }
   } else {
     // After the barrier that publishes a step, the stage before it is refilled
-    // with the step STAGES - 1 after it.  With four slices to a step half of
-    // the copies go between the products that follow the barrier and half
-    // between the next slice's, with two slices all between the former (all at
-    // once they block the waves; later ones land too late: a quarter later
-    // cost 2-4%).  The first fragments of a step are read before the last
-    // products of the one before.  Copies are issued under no condition (past
-    // the last tile they copy zeros): the compiler would move the products
-    // behind the branch.
+    // with the step STAGES - 1 after it: in two halves, between the products
+    // that follow the barrier and those of the next slice (all at once they
+    // block the waves; later ones land too late: a quarter later cost 2-4%);
+    // with two slices of microscaled operands, whose products take longer, all
+    // between the former.  The first fragments of a step are read before the
+    // last products of the one before.  Copies are issued under no condition
+    // (past the last tile they copy zeros): the compiler would move the
+    // products behind the branch.
     XFrag xf[2][FM];
     WFrag wf[2][FN];
-    constexpr int HALF = NS == 2 ? STEP_COPIES : STEP_COPIES / 2, PRODUCTS = FM * FN;
-    auto copies = [&](int to, auto first_, auto m_) {  // those of the half from `first` on that follow product m
-      constexpr int FIRST = decltype(first_)::value, M = decltype(m_)::value;
-      constexpr int COUNT = FIRST ? STEP_COPIES - HALF : HALF;
+    constexpr int PARTS = MX && NS == 2 ? 1 : 2, PRODUCTS = FM * FN;
+    auto copies = [&](int to, auto part_, auto m_) {  // those of a part that follow product m
+      constexpr int P = decltype(part_)::value, M = decltype(m_)::value;
+      constexpr int FIRST = STEP_COPIES * P / PARTS, COUNT = STEP_COPIES * (P + 1) / PARTS - FIRST;
       constexpr int A = FIRST + COUNT * M / PRODUCTS, B = FIRST + COUNT * (M + 1) / PRODUCTS;
       if constexpr (B > A) {
         __builtin_amdgcn_sched_barrier(0);
@@ -860,7 +876,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     };
     using First = std::integral_constant<int, 0>;
-    using Second = std::integral_constant<int, HALF>;
+    using Second = std::integral_constant<int, 1>;
     auto all_copies = [&](int to) {
       static_for<STEP_COPIES>([&](auto q_) { issue_copy(to, q_); });
       advance();
@@ -878,8 +894,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     for (int s = 0; s < STAGES - 1; ++s) all_copies(s);
     publish(0);
     issue_scales(1, 0);
-    static_for<HALF>([&](auto q_) { issue_copy(STAGES - 1, q_); });
-    if constexpr (HALF == STEP_COPIES) advance();
+    static_for<STEP_COPIES / PARTS>([&](auto q_) { issue_copy(STAGES - 1, q_); });
+    if constexpr (PARTS == 1) advance();
     fetch_scales(slot);
     read_frags(0, 0, xf[0], wf[0]);
     keep_scales();
@@ -890,7 +906,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         static_for<NS - 1>([&](auto s_) {
           constexpr int S = decltype(s_)::value;
           read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
-          if constexpr (S == 0 && HALF < STEP_COPIES) {
+          if constexpr (S == 0 && PARTS == 2) {
             multiply(xf[0], wf[0], s_, [&](auto m_) { copies(refill, Second{}, m_); });
             advance();
           } else {
@@ -920,7 +936,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         read_frags(st, 0, xf[0], wf[0]);
         multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{},
                  [&](auto m_) { copies(refill, First{}, m_); });
-        if constexpr (HALF == STEP_COPIES) advance();
+        if constexpr (PARTS == 1) advance();
         keep_scales();
       }
       epilogue(c);
@@ -1115,13 +1131,15 @@ void launch(const Plan& pl, hipStream_t s) {
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
   constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
   if (pl.kind == kLarge)
-    // the weight gradient's stages are whole rows of a tile whatever their
+    // The weight gradient's stages are whole rows of a tile whatever their
     // length: four short ones hide more of a copy's way than two long ones
     // (1.27 -> 1.20 ms at 32768 x 2048 x 7168); with rows along the reduction
-    // short stages would take half a line at a time (2-7% slower)
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK, 4, 2, WGRAD ? 4 : 2,
-                                       false, 2>),
-                       dim3(pl.grid), dim3(512), dyn, s, pl.p);
+    // short stages would take half a line at a time (2-7% slower).  Four waves
+    // of 128 x 128 read a third less from LDS than eight of 64 x 128, which
+    // transposing reads make up for (1.20 -> 1.12 ms; without them -1 .. +2%).
+    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK, WGRAD ? 2 : 4, 2,
+                                       WGRAD ? 4 : 2, false, WGRAD ? 1 : 2>),
+                       dim3(pl.grid), dim3(WGRAD ? 256 : 512), dyn, s, pl.p);
   else if (pl.kind == kMiddle)
     hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>), dim3(pl.grid),
                        dim3(256), dyn, s, pl.p);
