@@ -285,6 +285,9 @@ int gmm_finalize_routing_plan(const gmmfr_args* args, gmmfr_plan_info* info);
  *     token): shared exponent s = floor(log2(block amax)) - 8, clamped to
  *     [-127, 127] (-127 for an all-zero block), E8M0 code s + 127, codes of
  *     E4M3(clamp(x * 2^-s, -448, 448)).
+ * FP4 x1 with FLOAT8_E8M0 pertokenScale: the same with floor(log2(block amax))
+ *   - 2 and codes of E2M1(clamp(x * 2^-s, -6, 6)), two per byte, the lower
+ *   first (rows of gmm_grouped_matmul).
  *
  * Rows at and past sum(groupList counts) are not written (the grouped matmul
  * never reads them).  Hidden values must be finite; expert ids are device data
@@ -294,10 +297,12 @@ typedef struct {
   gmmfr_tensor hidden;         /* BFLOAT16 (T,k)                                required */
   gmmfr_tensor expert_ids;     /* INT32 or INT64 (T,K): global expert per slot  required */
   gmmfr_tensor topk_weights;   /* FLOAT32 (T,K) routing weights; given iff logit is given */
-  gmmfr_tensor x1;             /* out INT8 (T*K,k), or FLOAT8_E4M3FN (T*K,k)    required */
+  gmmfr_tensor x1;             /* out INT8 (T*K,k), FLOAT8_E4M3FN (T*K,k) or
+                                * FLOAT4_E2M1X2 (T*K,k/2)                      required */
   gmmfr_tensor pertoken_scale; /* out FLOAT32 (T*K); with FP8 x1 FLOAT32 (T*K), or
                                 * FLOAT8_E8M0 (T*K, k/64, 2): one scale per 32
-                                * values (MX; k % 64 == 0)                     required */
+                                * values (MX; k % 64 == 0); with FP4 x1 the
+                                * latter                                       required */
   gmmfr_tensor logit;          /* out FLOAT32 (T*K); given iff topk_weights is given      */
   gmmfr_tensor row_index;      /* out INT64 or INT32 (T*K)                      required */
   gmmfr_tensor group_list;     /* out INT64 (e)                                 required */

@@ -341,8 +341,9 @@ def quant_permute(hidden, expert_ids, num_experts: int, *, topk_weights=None, ex
                   stream=None) -> dict:
     """Allocate the outputs with torch and enqueue gmm_quant_permute on `stream`
     (default: the current stream).  mode: "int8" (int8 x1, fp32 per-token
-    scale), "fp8" (FP8 E4M3 x1, fp32 per-token scale) or "mx" (FP8 E4M3 x1,
-    E8M0 scale per 32 values, (m, k/64, 2)).  Returns the output tensors by name."""
+    scale), "fp8" (FP8 E4M3 x1, fp32 per-token scale), "mx" (FP8 E4M3 x1,
+    E8M0 scale per 32 values, (m, k/64, 2)) or "mx4" (FP4 E2M1 x1 (m, k/2),
+    scales as "mx").  Returns the output tensors by name."""
     import torch
     dev = hidden.device
     T, k = hidden.shape
@@ -365,6 +366,9 @@ def _quant_permute_on(hidden, expert_ids, num_experts, topk_weights, expert_offs
         pts = torch.empty(m, dtype=torch.float32, device=dev)
     elif mode == "mx":
         x1 = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=dev)
+        pts = torch.empty((m, k // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
+    elif mode == "mx4":
+        x1 = torch.empty((m, k // 2), dtype=torch.float4_e2m1fn_x2, device=dev)
         pts = torch.empty((m, k // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
     else:
         raise ValueError(f"unknown mode {mode!r}")

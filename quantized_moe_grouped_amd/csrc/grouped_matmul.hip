@@ -85,11 +85,13 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(
 // waits itself (wait_vmcnt) before the barrier that publishes a stage.  No
 // output registers; M0 is used by nothing else here.
 __device__ __forceinline__ void copy16(v4i r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+               "v"(off), "s"(r)
                : "memory");
 }
 __device__ __forceinline__ void copy4(v4i r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+               "v"(off), "s"(r)
                : "memory");
 }
 
@@ -899,17 +901,24 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     fetch_scales(slot);
     read_frags(0, 0, xf[0], wf[0]);
     keep_scales();
-    while (true) {
-      clear();
+    // The steps of a tile.  A wave whose rows all lie past the group's last
+    // (ALIVE false) only copies: where half of a tile's rows exist the waves
+    // that share its SIMDs have them alone (2% at 1024 rows an expert).
+    auto run = [&](auto alive_) {
+      constexpr bool ALIVE = decltype(alive_)::value;
+      auto with_copies = [&](XFrag (&x)[FM], WFrag (&w)[FN], auto s_, auto part_) {
+        if constexpr (ALIVE) multiply(x, w, s_, [&](auto m_) { copies(refill, part_, m_); });
+        else static_for<PRODUCTS>([&](auto m_) { copies(refill, part_, m_); });
+      };
 #pragma unroll 1
       for (int kt = 0; kt < steps; ++kt) {
         static_for<NS - 1>([&](auto s_) {
           constexpr int S = decltype(s_)::value;
-          read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+          if constexpr (ALIVE) read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
           if constexpr (S == 0 && PARTS == 2) {
-            multiply(xf[0], wf[0], s_, [&](auto m_) { copies(refill, Second{}, m_); });
+            with_copies(xf[0], wf[0], s_, Second{});
             advance();
-          } else {
+          } else if constexpr (ALIVE) {
             multiply(xf[S & 1], wf[S & 1], s_, nothing);
           }
         });
@@ -932,12 +941,28 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           }
           issue_scales(kt + 2 < steps ? kt + 2 : kt + 2 - steps, 0);
         }
+        if constexpr (ALIVE) {
+          fetch_scales(slot);
+          read_frags(st, 0, xf[0], wf[0]);
+        }
+        with_copies(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{}, First{});
+        if constexpr (PARTS == 1) advance();
+        if constexpr (ALIVE) keep_scales();
+      }
+      if constexpr (!ALIVE) {  // for the next tile
         fetch_scales(slot);
         read_frags(st, 0, xf[0], wf[0]);
-        multiply(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{},
-                 [&](auto m_) { copies(refill, First{}, m_); });
-        if constexpr (PARTS == 1) advance();
         keep_scales();
+      }
+    };
+    while (true) {
+      clear();
+      // (microscaled: the second form costs the first registers, and 8%)
+      if constexpr (MX || WGRAD) {
+        run(std::true_type{});
+      } else {
+        if (c.valid > wm * WTM) run(std::true_type{});
+        else run(std::false_type{});
       }
       epilogue(c);
       if (t_next < 0) break;

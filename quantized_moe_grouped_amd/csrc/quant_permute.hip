@@ -60,6 +60,7 @@ struct QpParams {
 constexpr int kQInt8 = 0;  // int8 per token, pertokenScale fp32 (m)
 constexpr int kQFp8 = 1;   // FP8 E4M3 per token, pertokenScale fp32 (m)
 constexpr int kQMx = 2;    // FP8 E4M3 with one E8M0 scale per 32 values, pertokenScale (m, k/64, 2)
+constexpr int kQMx4 = 3;   // FP4 E2M1, two per byte, scales as kQMx
 
 // Local expert of entry f, or -1 when its id lies outside [offset, offset+e)
 // (unsigned difference: no overflow for any id).
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(kQpThreads) void quant_rows_kernel(QpParams q) {
         fold(*(const uint4*)(row + c), *(const uint4*)(row + c + 8));
     }
     float inv = 0.0f;
-    if constexpr (QM != kQMx) {
+    if constexpr (QM != kQMx && QM != kQMx4) {
 #pragma unroll
       for (int off = 32; off >= 1; off >>= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, off));
       const float amax = bf16f(mag);
@@ -299,30 +300,46 @@ __global__ __launch_bounds__(kQpThreads) void quant_rows_kernel(QpParams q) {
         // block's shared exponent from its largest magnitude's bf16 exponent
         // field E (floor(log2) - 8, clamped at -127: E8M0 code max(E - 8, 0)),
         // codes of x * 2^(127 - code), saturated.
+        // MX FP4: the same with emax = 2 (E8M0 code max(E - 2, 0)) and the FP4
+        // conversion, which rounds to nearest even and saturates by itself.
+        constexpr bool kBlocks = QM == kQMx || QM == kQMx4;
+        constexpr uint32_t kEmax = QM == kQMx4 ? 2 : 8;
         int shift = 0;
         uint32_t bcode = 0;
-        if constexpr (QM == kQMx) {
+        if constexpr (kBlocks) {
           uint32_t bm = 0;
           const uint32_t wv[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) bm = max(bm, max(wv[i] & 0x7FFFu, (wv[i] >> 16) & 0x7FFFu));
           bm = max(bm, (uint32_t)__shfl_xor((int)bm, 1));
           const uint32_t ex = bm >> 7;
-          bcode = ex >= 8 ? ex - 8 : 0;
+          bcode = ex >= kEmax ? ex - kEmax : 0;
           shift = 127 - (int)bcode;
         }
-        auto enc4 = [&](uint32_t lo2, uint32_t hi2) {
-          const float x[4] = {bf16f(lo2 & 0xFFFFu), bf16f(lo2 >> 16), bf16f(hi2 & 0xFFFFu), bf16f(hi2 >> 16)};
-          uint32_t w = 0;
+        if constexpr (QM == kQMx4) {
+          const float scale = __uint_as_float(bcode ? bcode << 23 : 0x00400000u);
+          const uint32_t wv[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+          uint32_t d[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float t = QM == kQMx ? ldexpf(x[i], shift) : __fmul_rn(x[i], inv);
-            w |= e4m3_code(fminf(fmaxf(t, -448.0f), 448.0f)) << (8 * i);
-          }
-          return w;
-        };
-        o = u32x4{enc4(u.x, u.y), enc4(u.z, u.w), enc4(v.x, v.y), enc4(v.z, v.w)};
-        if constexpr (QM == kQMx) {
+          for (int i = 0; i < 8; ++i)
+            d[i >> 2] |= (__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, bf16f(wv[i] & 0xFFFFu), bf16f(wv[i] >> 16), scale, 0) &
+                          0xFFu)
+                         << (8 * (i & 3));
+          o = u32x4{d[0], d[1], 0, 0};
+        } else {
+          auto enc4 = [&](uint32_t lo2, uint32_t hi2) {
+            const float x[4] = {bf16f(lo2 & 0xFFFFu), bf16f(lo2 >> 16), bf16f(hi2 & 0xFFFFu), bf16f(hi2 >> 16)};
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float t = QM == kQMx ? ldexpf(x[i], shift) : __fmul_rn(x[i], inv);
+              w |= e4m3_code(fminf(fmaxf(t, -448.0f), 448.0f)) << (8 * i);
+            }
+            return w;
+          };
+          o = u32x4{enc4(u.x, u.y), enc4(u.z, u.w), enc4(v.x, v.y), enc4(v.z, v.w)};
+        }
+        if constexpr (kBlocks) {
           // the even lane of the pair writes the block's E8M0 code to each row
           if ((lane & 1) == 0) {
             for (int j = 0; j < q.K; ++j) {
@@ -334,7 +351,12 @@ __global__ __launch_bounds__(kQpThreads) void quant_rows_kernel(QpParams q) {
       }
       for (int j = 0; j < q.K; ++j) {
         const int32_t d = __builtin_amdgcn_readlane(dst, j);
-        if (d >= 0) __builtin_nontemporal_store(o, (u32x4*)(q.x1 + (int64_t)d * q.k + c));
+        if constexpr (QM == kQMx4) {
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          if (d >= 0) __builtin_nontemporal_store(u32x2{o.x, o.y}, (u32x2*)(q.x1 + ((int64_t)d * q.k + c) / 2));
+        } else {
+          if (d >= 0) __builtin_nontemporal_store(o, (u32x4*)(q.x1 + (int64_t)d * q.k + c));
+        }
       }
     };
     if constexpr (NI > 0) {
@@ -383,11 +405,13 @@ int qp_validate(const gmmqp_args* a, QpPlan* p) {
   if (a->expert_ids.dtype != GMMFR_DT_INT32 && a->expert_ids.dtype != GMMFR_DT_INT64) return GMMFR_ERR_DTYPE;
   if (given(a->topk_weights) && a->topk_weights.dtype != GMMFR_DT_FLOAT32) return GMMFR_ERR_DTYPE;
   // x1 INT8 with FLOAT32 per-token scales; FLOAT8_E4M3FN with FLOAT32 per-token
-  // scales, or with FLOAT8_E8M0 scales per 32 values (MX)
+  // scales, or with FLOAT8_E8M0 scales per 32 values (MX); FLOAT4_E2M1X2 with
+  // the latter
   int qmode;
   if (a->x1.dtype == GMMFR_DT_INT8 && a->pertoken_scale.dtype == GMMFR_DT_FLOAT32) qmode = kQInt8;
   else if (a->x1.dtype == GMMFR_DT_FLOAT8_E4M3FN && a->pertoken_scale.dtype == GMMFR_DT_FLOAT32) qmode = kQFp8;
   else if (a->x1.dtype == GMMFR_DT_FLOAT8_E4M3FN && a->pertoken_scale.dtype == GMMFR_DT_FLOAT8_E8M0) qmode = kQMx;
+  else if (a->x1.dtype == GMMFR_DT_FLOAT4_E2M1X2 && a->pertoken_scale.dtype == GMMFR_DT_FLOAT8_E8M0) qmode = kQMx4;
   else return GMMFR_ERR_DTYPE;
   if (given(a->logit) && a->logit.dtype != GMMFR_DT_FLOAT32) return GMMFR_ERR_DTYPE;
   if (a->row_index.dtype != GMMFR_DT_INT32 && a->row_index.dtype != GMMFR_DT_INT64) return GMMFR_ERR_DTYPE;
@@ -405,8 +429,8 @@ int qp_validate(const gmmqp_args* a, QpPlan* p) {
   const int64_t e = a->group_list.dims[0];
   if (e < 1 || e > kMaxLocalExperts) return GMMFR_ERR_SHAPE;
   if (given(a->topk_weights) && !shape_is(a->topk_weights, 2, T, K)) return GMMFR_ERR_SHAPE;
-  if (!shape_is(a->x1, 2, m, k) || !shape_is(a->row_index, 1, m)) return GMMFR_ERR_SHAPE;
-  if (qmode == kQMx) {
+  if (!shape_is(a->x1, 2, m, qmode == kQMx4 ? k / 2 : k) || !shape_is(a->row_index, 1, m)) return GMMFR_ERR_SHAPE;
+  if (qmode == kQMx || qmode == kQMx4) {
     const gmmfr_tensor& t = a->pertoken_scale;  // (m, k/64, 2): one E8M0 per 32 values
     if (k % 64 != 0 || t.ndim != 3 || t.dims[0] != m || t.dims[1] != k / 64 || t.dims[2] != 2) return GMMFR_ERR_SHAPE;
   } else if (!shape_is(a->pertoken_scale, 1, m)) {
@@ -478,7 +502,8 @@ int qp_run(const gmmqp_args* a, void* workspace, size_t workspace_bytes, void* s
       else if (p.k <= 4096) hipLaunchKernelGGL((quant_rows_kernel<4, QM>), dim3(qgrid), dim3(kQpThreads), 0, s, q);
       else hipLaunchKernelGGL((quant_rows_kernel<0, QM>), dim3(qgrid), dim3(kQpThreads), 0, s, q);
     };
-    if (p.qmode == kQMx) launch(std::integral_constant<int, kQMx>{});
+    if (p.qmode == kQMx4) launch(std::integral_constant<int, kQMx4>{});
+    else if (p.qmode == kQMx) launch(std::integral_constant<int, kQMx>{});
     else if (p.qmode == kQFp8) launch(std::integral_constant<int, kQFp8>{});
     else launch(std::integral_constant<int, kQInt8>{});
     if (events && events[1] && hipEventRecord((hipEvent_t)events[1], s) != hipSuccess) return GMMFR_ERR_HIP;

@@ -222,3 +222,22 @@ def test_python_entry_refuses_strided_tensors():
     x = torch.zeros((64, 8), dtype=torch.bfloat16).T
     with pytest.raises(ValueError):
         B.make_mq_args(x, x, x)
+
+
+def qp(x1, pts, k=2048, T=512, K=8):
+    a = B.QpArgs()
+    a.hidden, a.expert_ids, a.row_index, a.group_list = fake(BF, T, k), fake(I64, T, K), fake(I64, T * K), fake(I64, 32)
+    a.x1, a.pertoken_scale, a.group_list_type = x1, pts, 1
+    return a
+
+
+@pytest.mark.parametrize("a,code", [
+    (qp(fake(FP4, 4096, 1024), fake(E8, 4096, 32, 2)), B.OK),
+    (qp(fake(FP4, 4096, 1024), fake(F32, 4096)), B.ERR_DTYPE),
+    (qp(fake(FP4, 4096, 2048), fake(E8, 4096, 32, 2)), B.ERR_SHAPE),
+    (qp(fake(FP4, 4096, 1024), fake(E8, 4096, 64)), B.ERR_SHAPE),
+    (qp(fake(FP4, 4096, 1040), fake(E8, 4096, 32, 2), k=2080), B.ERR_SHAPE),
+], ids=["ok", "scale_dtype", "codes_unpacked", "scale_shape", "k_not_mult_64"])
+def test_producer_step_with_fp4_rows(a, code):
+    st, _ = stage_one("gmm_quant_permute", a)
+    assert st == code
