@@ -275,7 +275,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // (workgroup b runs on XCD b % 8), at most 64 a block and fewer when there
   // are few tiles, so that every XCD gets some
   const int G = gridDim.x;
-  const int block = min(64, (total + kXcds - 1) / kXcds);
+  const int block = max(1, min(64, (total + kXcds - 1) / kXcds));
   auto tile_at = [&](int j) -> int {
     int64_t t;
     if (G % kXcds == 0) {
@@ -1060,6 +1060,8 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   if (tuning(a->tuning_config, a->tuning_config_len, &rows, &height, &cap) != GMMFR_OK) return GMMFR_ERR_ATTR;
   const bool glu = a->activation == GMMGM_ACT_SWIGLU;
   if (a->x.ndim != 2 || a->w.ndim != 3 || a->group_list.ndim != 1) return GMMFR_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if ((i < 2 && a->x.dims[i] >= (int64_t(1) << 31)) || a->w.dims[i] >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
   const int per = xt == GMMFR_DT_FLOAT4_E2M1X2 ? 2 : 1, wper = mx ? 2 : 1;  // values an element of the shape stands for
   const int64_t m = a->x.dims[0], k = a->x.dims[1] * per, e = a->w.dims[0];
   const int64_t n = a->w.dims[a->transpose_w ? 1 : 2], wk = a->w.dims[a->transpose_w ? 2 : 1] * wper;

@@ -336,3 +336,76 @@ def test_results_do_not_depend_on_the_grid():
         first = B.grouped_matmul(x, w, gl, group_list_type=1, tuning_config=[0, height])
         for cap in (1, 7, 64):
             assert torch.equal(first, B.grouped_matmul(x, w, gl, group_list_type=1, tuning_config=[0, height, cap]))
+
+
+@pytest.mark.parametrize("height", [32, 128, 256])
+def test_groups_without_any_row(height):
+    """m > 0 and every group empty: nothing is written; the weight gradient is zero."""
+    x = torch.ones((50, 64), dtype=BF16, device="cuda")
+    w = torch.ones((3, 64, 32), dtype=BF16, device="cuda")
+    gl = torch.zeros(3, dtype=torch.int64, device="cuda")
+    out = torch.full((50, 32), SENTINEL, dtype=BF16, device="cuda")
+    for list_type in (0, 1):
+        B.grouped_matmul(x, w, gl, out=out, group_list_type=list_type, tuning_config=[0, height])
+        assert (out == SENTINEL).all()
+        if height > 32:
+            dw = B.grouped_matmul_wgrad(x, x[:, :32].contiguous(), gl, group_list_type=list_type, tuning_config=[0, height])
+            assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("height", [32, 128, 256])
+def test_as_many_experts_as_allowed(height):
+    _dense_case(21, 3000, 1024, 72, 40, BF16, BF16, False, None, 1, 2, tuning=[0, height], empty=0.4)
+    for fmt in ("fp4", "fp8"):
+        _mx_case(22, 3000, 1024, 128, 48, fmt, BF16, None, 0, 2, tuning=[0, height], empty=0.4)
+
+
+def test_weight_gradient_of_as_many_experts_as_allowed():
+    rng = np.random.default_rng(23)
+    m, e, k, n = 3000, 1024, 24, 40
+    counts = R.counts_for(rng, m, e, 0.4)
+    x, dy = _rand(rng, (m, k), BF16), _rand(rng, (m, n), BF16)
+    want, s, rows = R.wgrad(x.double(), dy.double(), counts, 1)
+    bound = s * (rows + 1)[:, None, None] * R.U
+    for height in (128, 256):
+        dw = B.grouped_matmul_wgrad(x.cuda(), dy.cuda(), torch.from_numpy(counts).cuda(), group_list_type=1,
+                                    tuning_config=[0, height])
+        R.assert_within(dw, want, bound + R.half_step(want.abs() + bound, F32), f"height {height}")
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("height", [32, 128, 256])
+def test_nan_scales_stay_in_their_row_or_column(fmt, height):
+    rng = np.random.default_rng(24)
+    m, e, k, n = 300, 2, 1088, 272
+    x, xs = _mx_operand(rng, (m, k), fmt)
+    w, ws = _mx_operand(rng, (e, n, k), "fp4")
+    xs.view(torch.uint8)[11, 16, 0] = 255
+    xs.view(torch.uint8)[12, 0, 0] = 255
+    ws.view(torch.uint8)[1, 5, 16, 1] = 255
+    y = B.grouped_matmul(x.cuda(), w.cuda(), torch.tensor([100, 200]).cuda(), x_scale=xs.cuda(), w_scale=ws.cuda(),
+                         transpose_w=True, group_list_type=1, tuning_config=[0, height]).float().cpu()
+    bad = torch.zeros((m, n), dtype=torch.bool)
+    bad[11] = bad[12] = True
+    bad[100:, 5] = True
+    assert torch.equal(torch.isnan(y), bad)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_drawn_products(seed):
+    """Shapes, layouts, types, tiles and group lists drawn over small ranges."""
+    rng = np.random.default_rng(1000 + seed)
+    m, e = int(rng.integers(1, 900)), int(rng.integers(1, 40))
+    height, cap = int(rng.choice([0, 32, 128, 256])), int(rng.choice([0, 0, 5, 40]))
+    spare = int(rng.integers(0, min(m, 9)))
+    act = [None, "swiglu"][rng.integers(2)]
+    list_type = int(rng.integers(2))
+    if rng.random() < 0.5:
+        k, n = 8 * int(rng.integers(1, 90)), 16 * int(rng.integers(1, 50))
+        dtype = [BF16, F16][rng.integers(2)]
+        _dense_case(seed, m, e, k, n, dtype, [dtype, F32][rng.integers(2)], bool(rng.integers(2)), act, list_type, spare,
+                    tuning=[0, height, cap])
+    else:
+        k, n = 64 * int(rng.integers(1, 30)), 16 * int(rng.integers(1, 50))
+        _mx_case(seed, m, e, k, n, ["fp4", "fp8"][rng.integers(2)], [BF16, F16, F32][rng.integers(3)], act, list_type,
+                 spare, tuning=[0, height, cap])
