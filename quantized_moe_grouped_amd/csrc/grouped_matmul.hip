@@ -202,6 +202,7 @@ struct Tile {
   int valid;   // rows of the tile that exist
   int n0;      // first column (SwiGLU: of y)
   int r0, r1;  // the reduction's range (wgrad: the group's rows)
+  bool alone;  // the group has no other tile along M
 };
 
 template <int N, int I = 0, typename F>
@@ -324,6 +325,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     c.n0 = nt * (GLU ? BN / 2 : BN);
     c.r0 = WGRAD ? begin : 0;
     c.r1 = WGRAD ? end : (int)p.k;
+    c.alone = mtiles == 1;
     return c;
   };
   auto steps_of = [&](const Tile& c) -> int {
@@ -350,6 +352,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const uint8_t* ws_at = nullptr;
   uint32_t x_size = 0, w_size = 0, xs_size = 0, ws_size = 0;
   int r_left = 0;                  // of the reduction, from the step on
+  bool w_once = false;             // KWAVES: no other tile reads these weights
   uint32_t x_skip = 0, w_skip = 0; // rows across the reduction: bytes of a row before the tile
   uint32_t x_off[XI], w_off[WI], s_off[2] = {kOutside, kOutside}, s_odd[2] = {0, 0};
   const int x_ch = XCOL ? 0 : ((lane % XC) ^ swz_row<XC>(tid / XC)) * 16;
@@ -361,6 +364,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     int lane = threadIdx.x & 63, tid = threadIdx.x;
     asm volatile("" : "+v"(lane), "+v"(tid));
     r_left = c.r1 - c.r0;
+    w_once = c.alone;
     if constexpr (XCOL) {  // wgrad: from (first row of the group, first column of the tile)
       x_skip = c.m0 * 2;
       x_at = (const uint8_t*)p.x + (int64_t)c.r0 * x_row + x_skip;
@@ -507,8 +511,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       const v4i wr = buffer(w_at, WCOL ? across((uint32_t)w_row, w_skip) : w_size);
       const uint32_t off = WCOL || w_ch * 8 / WBITS < r_left ? w_off[Q - XI] : kOutside;
       const uint32_t to = __builtin_amdgcn_readfirstlane(lds_addr(sW)) + st * W_BYTES + ((Q - XI) * NWAVES + wave) * 1024;
-      // (one token through bf16 experts 50.5 -> 47.7 us; microscaled ones alike)
-      if constexpr (KWAVES && !MX) copy16_once(wr, off, to);
+      // (one token through bf16 experts 50.5 -> 47.7 us; microscaled ones
+      // alike.  Where a group has several tiles the others find the weights in
+      // the L2: 48 rows an expert 350 -> 274 us)
+      if (KWAVES && !MX && w_once) copy16_once(wr, off, to);
       else copy16(wr, off, to);
     }
   };
@@ -1108,12 +1114,24 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   pl->glu = glu;
   pl->col = a->transpose_w == 0;
   // Rows an expert is likely to have (experts without rows cost nothing), and
-  // half a tile of each expert's cut short.  Up to 32 rows the narrow tiles
-  // that stream the weights (256 experts of 8 rows on average: 0.52 against
-  // 0.55 ms with 128-row tiles; 32 of 128: 0.45 against 0.27).
+  // half a tile of each expert's cut short.  Few rows: the narrow tiles, which
+  // stream the weights (us, narrow against 128-row; e experts, k = 7168):
+  //   FP8, n = 4096      e = 64:   32 rows 275, 319   40 rows 328, 280
+  //   FP4, n = 2048      e = 32:   12 rows  52,  56   24 rows  68,  57
+  //   (e,n,k), n = 2048  e = 32:   12 rows 147, 166   24 rows 188, 169
+  // While the 128-row tiles leave CUs idle, up to 32 rows in all of them:
+  //   FP4, n = 2048      e = 16:   32 rows  39,  40   e = 8:  22,  35
+  //   (e,n,k), n = 2048  e = 16:   24 rows 124, 128   e = 8:  63, 103
+  // Weights (e,k,n), of which a narrow tile takes half as much of a row at a
+  // time, only then:
+  //   (e,k,n), n = 2048  e = 32:   12 rows 181, 168   e = 16: 91, 116
+  //   (e,k,n), n = 2048  e = 16:   24 rows 147, 117   e = 8:  77,  98
   const int64_t parts = e < m ? e : m, avg = rows > 0 ? rows : m / (parts > 0 ? parts : 1);
+  const int64_t middle = parts * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
+  const bool narrow = avg <= 16 ? !pl->col || middle <= 256
+                                : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256));
   pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
-                    : (avg <= 32 ? kSmall : larger_kind(2 * m / 256 + parts, 2 * m / 128 + parts, n));
+                    : (narrow ? kSmall : larger_kind(2 * m / 256 + parts, 2 * m / 128 + parts, n));
   const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
   p.tiles_m = 0;
   p.tiles_n = (int32_t)ceil_div(glu ? n / 2 : n, tn);
