@@ -35,7 +35,7 @@
 //   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.91 ms,
 //     1.06 PFLOP/s.  Matrix cores busy 64% of the cycles at the 1.74 GHz that
 //     the card's power leaves; between them the waits for LDS and barriers.
-//   - weight gradient of the same: 1.14 ms, 45% busy at 1.88 GHz: one
+//   - weight gradient of the same: 1.11 ms, 45% busy at 1.88 GHz: one
 //     workgroup a CU (its sums fill the registers), whose 1.9 GB of fp32
 //     results nothing else covers.
 //   - FP4, 131072 x 7168 x 4096 over 32, SwiGLU: 2.05 ms, 3.75 PFLOP/s: a
@@ -296,10 +296,12 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const bool s_split = MX && (s_row & 3) != 0;  // k % 128 == 64: odd rows' scales begin mid-dword
 
   // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
-  // (workgroup b runs on XCD b % 8), at most 64 a block and fewer when there
-  // are few tiles, so that every XCD gets some
+  // (workgroup b runs on XCD b % 8), as many a block as its 32 CUs run at once
+  // (with 64 of the 256-row tiles an XCD may have two rounds left where others
+  // have none: FP8 ragged 638 -> 609 us, weight gradients 2-10%) and fewer
+  // when there are few tiles, so that every XCD gets some
   const int G = gridDim.x;
-  const int block = max(1, min(64, (total + kXcds - 1) / kXcds));
+  const int block = max(1, min(BM >= 256 ? 32 : 64, (total + kXcds - 1) / kXcds));
   auto tile_at = [&](int j) -> int {
     int64_t t;
     if (G % kXcds == 0) {
