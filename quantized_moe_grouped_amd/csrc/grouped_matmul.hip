@@ -1058,11 +1058,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // 256-row tiles or 128-row ones, of which `large` and `middle` (in halves) lie
 // along M: by the rounds of the chip that they make, a round of 512 small
-// tiles (two a CU) taking 0.6 of a round of 256 large ones (measured at 32768 x
-// 2048 x 7168 over 32 experts: 1.15 against 0.95 ms for the same work).
-Kind larger_kind(int64_t large, int64_t middle, int64_t columns) {
+// tiles (two a CU) taking 0.6 of a round of 256 large ones, 0.65 with
+// microscaled operands (measured at 32768 x 2048 x 7168 over 32 experts, 16
+// bit: 1.15 against 0.95 ms for the same work; FP4, 12000 x 7168 x 4096 over
+// 64: 8 rounds in 0.41 ms against 5 in 0.34).
+Kind larger_kind(int64_t large, int64_t middle, int64_t columns, bool mx) {
   const int64_t l = ceil_div(large * ceil_div(columns, 256), 2 * 256), m = ceil_div(middle * ceil_div(columns, 128), 2 * 512);
-  return l * 10 <= m * 6 ? kLarge : kMiddle;
+  return l * 100 <= m * (mx ? 65 : 60) ? kLarge : kMiddle;
 }
 
 int grid_of(const Plan& pl, int64_t tiles, int64_t cap) {
@@ -1131,9 +1133,9 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : xt == GMMFR_DT_FLOAT16 ? kF16 : per == 2 ? kFp4 : kFp8;
   pl->glu = glu;
   pl->col = a->transpose_w == 0;
-  // Rows an expert is likely to have (experts without rows cost nothing), and
-  // half a tile of each expert's cut short.  Few rows: the narrow tiles, which
-  // stream the weights (us, narrow against 128-row; e experts, k = 7168):
+  // By the rows an expert is likely to have (experts without rows cost
+  // nothing).  Few rows: the narrow tiles, which stream the weights (us, narrow
+  // against 128-row; e experts, k = 7168):
   //   FP8, n = 4096      e = 64:   32 rows 275, 319   40 rows 328, 280
   //   FP4, n = 2048      e = 32:   12 rows  52,  56   24 rows  68,  57
   //   (e,n,k), n = 2048  e = 32:   12 rows 147, 166   24 rows 188, 169
@@ -1144,12 +1146,17 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   // time, only then:
   //   (e,k,n), n = 2048  e = 32:   12 rows 181, 168   e = 16: 91, 116
   //   (e,k,n), n = 2048  e = 16:   24 rows 147, 117   e = 8:  77,  98
+  // Tiles along M, in halves, for the choice among the others: one an expert up
+  // to three quarters of a tile, then half a tile of each cut short (bf16, 64
+  // experts of 188 rows, 2048 x 7168: 606 us with half a tile cut always, 501 so;
+  // FP8 315 and 258, and with much skewed groups 299 and 302).
   const int64_t parts = e < m ? e : m, avg = rows > 0 ? rows : m / (parts > 0 ? parts : 1);
   const int64_t middle = parts * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
   const bool narrow = avg <= 16 ? !pl->col || middle <= 256
                                 : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256));
+  auto along = [&](int64_t t) { return 4 * m <= 3 * t * parts ? 2 * parts : 2 * m / t + parts; };
   pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
-                    : (narrow ? kSmall : larger_kind(2 * m / 256 + parts, 2 * m / 128 + parts, n));
+                    : (narrow ? kSmall : larger_kind(along(256), along(128), n, mx));
   const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
   p.tiles_m = 0;
   p.tiles_n = (int32_t)ceil_div(glu ? n / 2 : n, tn);
@@ -1195,7 +1202,7 @@ int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   pl->glu = false;
   pl->col = true;
   pl->kind = height ? (height == 256 ? kLarge : kMiddle)
-                    : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n);
+                    : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n, false);
   p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);
   p.tiles_n = (int32_t)ceil_div(n, kTileN[pl->kind]);
   pl->grid = grid_of(*pl, e * p.tiles_m * p.tiles_n, cap);
