@@ -46,6 +46,7 @@ struct Params {
   int64_t chunks;   // 8-value chunks in all (rows), or 0
   int64_t k, n;     // columns kernel
   int64_t tiles_k, tiles_n;
+  int64_t first;    // workgroups of the launches before this one
 };
 
 template <int IN>
@@ -100,7 +101,7 @@ constexpr int kThreads = 256, kPer = 2;  // chunks of a thread, kThreads apart
 
 template <int IN, bool FP8>
 __global__ __launch_bounds__(kThreads) void quant_rows_kernel(Params p) {
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * kPer) + threadIdx.x;
+  const int64_t first = (p.first + blockIdx.x) * (kThreads * kPer) + threadIdx.x;
   float v[kPer][8];
 #pragma unroll
   for (int u = 0; u < kPer; ++u)
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void quant_cols_kernel(Params p) {
   __shared__ __attribute__((aligned(16))) uint8_t s_codes[kColN * kRow];
   __shared__ __attribute__((aligned(16))) uint8_t s_scales[kColN * 8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t per = p.tiles_k * p.tiles_n, g = blockIdx.x / per, t = blockIdx.x % per;
+  const int64_t per = p.tiles_k * p.tiles_n, at_tile = p.first + blockIdx.x, g = at_tile / per, t = at_tile % per;
   const int64_t k0 = (t % p.tiles_k) * kColK, n0 = (t / p.tiles_k) * kColN;
   const int64_t col = n0 + 2 * lane;
   const int blocks = (int)min((int64_t)8, (p.k - k0) / 32);
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(kThreads) void quant_cols_kernel(Params p) {
 
 template <int OUT, bool FP8>
 __global__ __launch_bounds__(kThreads) void dequant_kernel(Params p) {
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * kPer) + threadIdx.x;
+  const int64_t first = (p.first + blockIdx.x) * (kThreads * kPer) + threadIdx.x;
   v2u d[kPer];
   uint32_t s[kPer];
 #pragma unroll
@@ -316,6 +317,18 @@ void with(int in, bool fp8, F&& f) {
   else go(std::integral_constant<int, kF32>{});
 }
 
+// A launch holds fewer than 2^32 threads (more are dropped without an error):
+// `groups` workgroups in launches of at most 2^23.
+template <typename F>
+void in_launches(int64_t groups, Params* p, F&& launch) {
+  constexpr int64_t kMost = int64_t(1) << 23;
+  static_assert(kMost * kThreads < (int64_t(1) << 32), "threads of a launch");
+  for (p->first = 0; p->first < groups; p->first += kMost) {
+    const int64_t left = groups - p->first;
+    launch(dim3((uint32_t)(left < kMost ? left : kMost)));
+  }
+}
+
 int quantize(const gmmmq_args* a, void* stream) {
   Params p;
   int in;
@@ -324,15 +337,16 @@ int quantize(const gmmmq_args* a, void* stream) {
   const int st = validate(a, false, &p, &in, &fp8, &e);
   if (st != GMMFR_OK) return st;
   if (p.chunks == 0) return GMMFR_OK;
-  const int64_t grid = a->transpose ? e * p.tiles_k * p.tiles_n : (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
-  if (grid >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
+  const int64_t groups = a->transpose ? e * p.tiles_k * p.tiles_n : (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
   with(in, fp8, [&](auto in_, auto fp8_) {
-    if (a->transpose)
-      hipLaunchKernelGGL((quant_cols_kernel<decltype(in_)::value, decltype(fp8_)::value>), dim3((uint32_t)grid),
-                         dim3(kThreads), 0, (hipStream_t)stream, p);
-    else
-      hipLaunchKernelGGL((quant_rows_kernel<decltype(in_)::value, decltype(fp8_)::value>), dim3((uint32_t)grid),
-                         dim3(kThreads), 0, (hipStream_t)stream, p);
+    in_launches(groups, &p, [&](dim3 grid) {
+      if (a->transpose)
+        hipLaunchKernelGGL((quant_cols_kernel<decltype(in_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
+                           (hipStream_t)stream, p);
+      else
+        hipLaunchKernelGGL((quant_rows_kernel<decltype(in_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
+                           (hipStream_t)stream, p);
+    });
   });
   return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
 }
@@ -345,11 +359,12 @@ int dequantize(const gmmmq_args* a, void* stream) {
   const int st = validate(a, true, &p, &out, &fp8, &e);
   if (st != GMMFR_OK) return st;
   if (p.chunks == 0) return GMMFR_OK;
-  const int64_t grid = (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
-  if (grid >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
+  const int64_t groups = (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
   with(out, fp8, [&](auto out_, auto fp8_) {
-    hipLaunchKernelGGL((dequant_kernel<decltype(out_)::value, decltype(fp8_)::value>), dim3((uint32_t)grid),
-                       dim3(kThreads), 0, (hipStream_t)stream, p);
+    in_launches(groups, &p, [&](dim3 grid) {
+      hipLaunchKernelGGL((dequant_kernel<decltype(out_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
+                         (hipStream_t)stream, p);
+    });
   });
   return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
 }
