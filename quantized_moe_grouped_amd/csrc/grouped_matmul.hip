@@ -1235,11 +1235,14 @@ int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   return GMMFR_OK;
 }
 
+// (hipLaunchKernel gives this launch's own status, where the runtime's last
+// error may be an earlier one of the program's)
 template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU>
-void launch(const Plan& pl, hipStream_t s) {
+hipError_t launch(Plan& pl, hipStream_t s) {
   const size_t dyn = (size_t)(2 * pl.p.e + 1) * 4;
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
   constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
+  void* args[] = {&pl.p};
   if (pl.kind == kLarge)
     // The weight gradient's stages are whole rows of a tile whatever their
     // length: four short ones hide more of a copy's way than two long ones
@@ -1247,15 +1250,16 @@ void launch(const Plan& pl, hipStream_t s) {
     // short stages would take half a line at a time (2-7% slower).  Four waves
     // of 128 x 128 read a third less from LDS than eight of 64 x 128, which
     // transposing reads make up for (1.20 -> 1.12 ms; without them -1 .. +2%).
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK, WGRAD ? 2 : 4, 2,
-                                       WGRAD ? 4 : 2, false, WGRAD ? 1 : 2>),
-                       dim3(pl.grid), dim3(WGRAD ? 256 : 512), dyn, s, pl.p);
-  else if (pl.kind == kMiddle)
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>), dim3(pl.grid),
-                       dim3(256), dyn, s, pl.p);
-  else if constexpr (!WGRAD)
-    hipLaunchKernelGGL((product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, STS, true, 2>), dim3(pl.grid),
-                       dim3(256), dyn, s, pl.p);
+    return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK,
+                                                       WGRAD ? 2 : 4, 2, WGRAD ? 4 : 2, false, WGRAD ? 1 : 2>,
+                           dim3(pl.grid), dim3(WGRAD ? 256 : 512), args, dyn, s);
+  if constexpr (!WGRAD) {
+    if (pl.kind == kSmall)
+      return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, STS, true, 2>,
+                             dim3(pl.grid), dim3(256), args, dyn, s);
+  }
+  return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 128, 128, BK, 2, 2, 2, false, 2>,
+                         dim3(pl.grid), dim3(256), args, dyn, s);
 }
 
 int product_run(const gmmgm_args* a, void* stream) {
@@ -1264,24 +1268,19 @@ int product_run(const gmmgm_args* a, void* stream) {
   if (st != GMMFR_OK) return st;
   if (pl.p.m == 0) return GMMFR_OK;
   hipStream_t s = (hipStream_t)stream;
-  auto with = [&](auto enc_) {
+  auto with = [&](auto enc_) -> hipError_t {
     constexpr int ENC = decltype(enc_)::value;
     constexpr bool MX = ENC == kFp4 || ENC == kFp8;
     if constexpr (!MX) {
-      if (pl.col) {
-        if (pl.glu) launch<ENC, false, true, false, true>(pl, s);
-        else launch<ENC, false, true, false, false>(pl, s);
-        return;
-      }
+      if (pl.col) return pl.glu ? launch<ENC, false, true, false, true>(pl, s) : launch<ENC, false, true, false, false>(pl, s);
     }
-    if (pl.glu) launch<ENC, false, false, false, true>(pl, s);
-    else launch<ENC, false, false, false, false>(pl, s);
+    return pl.glu ? launch<ENC, false, false, false, true>(pl, s) : launch<ENC, false, false, false, false>(pl, s);
   };
-  if (pl.enc == kBf16) with(std::integral_constant<int, kBf16>{});
-  else if (pl.enc == kF16) with(std::integral_constant<int, kF16>{});
-  else if (pl.enc == kFp4) with(std::integral_constant<int, kFp4>{});
-  else with(std::integral_constant<int, kFp8>{});
-  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+  const hipError_t done = pl.enc == kBf16   ? with(std::integral_constant<int, kBf16>{})
+                          : pl.enc == kF16  ? with(std::integral_constant<int, kF16>{})
+                          : pl.enc == kFp4  ? with(std::integral_constant<int, kFp4>{})
+                                            : with(std::integral_constant<int, kFp8>{});
+  return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
 }
 
 int wgrad_run(const gmmgw_args* a, void* stream) {
@@ -1289,9 +1288,8 @@ int wgrad_run(const gmmgw_args* a, void* stream) {
   const int st = wgrad_plan(a, &pl);
   if (st != GMMFR_OK) return st;
   hipStream_t s = (hipStream_t)stream;
-  if (pl.enc == kBf16) launch<kBf16, true, true, true, false>(pl, s);
-  else launch<kF16, true, true, true, false>(pl, s);
-  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+  const hipError_t done = pl.enc == kBf16 ? launch<kBf16, true, true, true, false>(pl, s) : launch<kF16, true, true, true, false>(pl, s);
+  return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
 }
 
 }  // namespace gmmgm

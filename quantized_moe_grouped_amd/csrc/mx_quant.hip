@@ -318,15 +318,19 @@ void with(int in, bool fp8, F&& f) {
 }
 
 // A launch holds fewer than 2^32 threads (more are dropped without an error):
-// `groups` workgroups in launches of at most 2^23.
-template <typename F>
-void in_launches(int64_t groups, Params* p, F&& launch) {
+// `groups` workgroups in launches of at most 2^23.  hipLaunchKernel gives each
+// launch's own status, where the runtime's last error may be an earlier one of
+// the program's.
+int in_launches(const void* kernel, int64_t groups, Params p, void* stream) {
   constexpr int64_t kMost = int64_t(1) << 23;
   static_assert(kMost * kThreads < (int64_t(1) << 32), "threads of a launch");
-  for (p->first = 0; p->first < groups; p->first += kMost) {
-    const int64_t left = groups - p->first;
-    launch(dim3((uint32_t)(left < kMost ? left : kMost)));
+  void* args[] = {&p};
+  for (p.first = 0; p.first < groups; p.first += kMost) {
+    const int64_t left = groups - p.first;
+    const dim3 grid((uint32_t)(left < kMost ? left : kMost));
+    if (hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, (hipStream_t)stream) != hipSuccess) return GMMFR_ERR_HIP;
   }
+  return GMMFR_OK;
 }
 
 int quantize(const gmmmq_args* a, void* stream) {
@@ -336,19 +340,13 @@ int quantize(const gmmmq_args* a, void* stream) {
   int64_t e;
   const int st = validate(a, false, &p, &in, &fp8, &e);
   if (st != GMMFR_OK) return st;
-  if (p.chunks == 0) return GMMFR_OK;
-  const int64_t groups = a->transpose ? e * p.tiles_k * p.tiles_n : (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
+  const void* kernel = nullptr;
   with(in, fp8, [&](auto in_, auto fp8_) {
-    in_launches(groups, &p, [&](dim3 grid) {
-      if (a->transpose)
-        hipLaunchKernelGGL((quant_cols_kernel<decltype(in_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
-                           (hipStream_t)stream, p);
-      else
-        hipLaunchKernelGGL((quant_rows_kernel<decltype(in_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
-                           (hipStream_t)stream, p);
-    });
+    kernel = a->transpose ? (const void*)quant_cols_kernel<decltype(in_)::value, decltype(fp8_)::value>
+                          : (const void*)quant_rows_kernel<decltype(in_)::value, decltype(fp8_)::value>;
   });
-  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+  const int64_t groups = a->transpose ? e * p.tiles_k * p.tiles_n : (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
+  return in_launches(kernel, groups, p, stream);
 }
 
 int dequantize(const gmmmq_args* a, void* stream) {
@@ -358,15 +356,11 @@ int dequantize(const gmmmq_args* a, void* stream) {
   int64_t e;
   const int st = validate(a, true, &p, &out, &fp8, &e);
   if (st != GMMFR_OK) return st;
-  if (p.chunks == 0) return GMMFR_OK;
-  const int64_t groups = (p.chunks + kThreads * kPer - 1) / (kThreads * kPer);
+  const void* kernel = nullptr;
   with(out, fp8, [&](auto out_, auto fp8_) {
-    in_launches(groups, &p, [&](dim3 grid) {
-      hipLaunchKernelGGL((dequant_kernel<decltype(out_)::value, decltype(fp8_)::value>), grid, dim3(kThreads), 0,
-                         (hipStream_t)stream, p);
-    });
+    kernel = (const void*)dequant_kernel<decltype(out_)::value, decltype(fp8_)::value>;
   });
-  return hipGetLastError() == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+  return in_launches(kernel, (p.chunks + kThreads * kPer - 1) / (kThreads * kPer), p, stream);
 }
 
 }  // namespace gmmmq
