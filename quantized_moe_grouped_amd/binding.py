@@ -467,13 +467,22 @@ def make_mq_args(x, codes, scales, *, transpose: bool = False):
     return MqArgs.from_buffer_copy(_mq_bytes(x, codes, scales, transpose)), (x, codes, scales)
 
 
-def _check_device(dev, *tensors) -> None:
-    """The kernels dereference these pointers on `dev`: all tensors live there."""
+def _check_tensors(x, *others):
+    """The device of x.  No tensor may want a gradient that these calls would
+    lose (they record no history), and all live on one GPU, where the kernels
+    dereference their pointers."""
+    import torch
+    tensors = [t for t in (x, *others) if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError("these calls record no gradients: detach the tensors, or call them under torch.no_grad() or in "
+                         "a torch.autograd.Function of your own")
+    dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {dev}")
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t.device != dev:
             raise ValueError(f"tensors must be on one device: {t.device} and {dev}")
+    return dev
 
 
 def _on(dev, stream, call, *args):
@@ -516,9 +525,10 @@ def grouped_matmul(x, w, group_list, *, x_scale=None, w_scale=None, out=None, ou
     with (e,k,n) weights), or microscaled x (FP8 or FP4) and FP4 w (e,n,k) with
     their scales.  Returns out, allocated as (m, n or n/2) if none is given, in
     out_dtype (default: x's type; bf16 for microscaled x); rows behind the last
-    group are left as they are."""
-    _check_device(x.device, w, group_list, x_scale, w_scale, out, workspace)
-    return _on(x.device, stream, _grouped_matmul, x, w, group_list, x_scale, w_scale, out, out_dtype, group_list_type,
+    group are left as they are.  Records no history: tensors that want a
+    gradient are refused (see also grouped_matmul_wgrad)."""
+    dev = _check_tensors(x, w, group_list, x_scale, w_scale, out, workspace)
+    return _on(dev, stream, _grouped_matmul, x, w, group_list, x_scale, w_scale, out, out_dtype, group_list_type,
                transpose_w, activation, tuning_config, workspace)
 
 
@@ -541,11 +551,13 @@ def grouped_matmul_wgrad(x, dy, group_list, *, out=None, out_dtype=None, accumul
                          stream=None):
     """Gradient of a grouped product's weights (e,k,n): x_g^T dy_g for every
     expert, in out_dtype (default fp32), zeros for one without rows.
-    accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x)."""
-    _check_device(x.device, dy, group_list, out, workspace)
+    accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x).
+    With activation "swiglu" dy is the gradient of the product before it, which
+    no call here makes of the gradient behind it."""
+    dev = _check_tensors(x, dy, group_list, out, workspace)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    return _on(x.device, stream, _grouped_matmul_wgrad, x, dy, group_list, out, out_dtype, accumulate,
+    return _on(dev, stream, _grouped_matmul_wgrad, x, dy, group_list, out, out_dtype, accumulate,
                group_list_type, tuning_config, workspace)
 
 
@@ -570,8 +582,7 @@ def mx_quantize(x, *, format: str = "fp4", transpose: bool = False, stream=None)
         raise ValueError(f"unknown format {format!r}")
     if transpose and x.dim() != 3:
         raise ValueError("transpose takes weights (e,k,n)")
-    _check_device(x.device)
-    return _on(x.device, stream, _mx_quantize, x, format, transpose)
+    return _on(_check_tensors(x), stream, _mx_quantize, x, format, transpose)
 
 
 def _mx_quantize(handle, x, format, transpose):
@@ -592,8 +603,7 @@ def _mx_quantize(handle, x, format, transpose):
 def mx_dequantize(codes, scales, *, dtype=None, stream=None):
     """The values that codes and scales stand for, (rows,k) or (e,n,k), in
     dtype (bf16 by default, fp16 or fp32)."""
-    _check_device(codes.device, scales)
-    return _on(codes.device, stream, _mx_dequantize, codes, scales, dtype)
+    return _on(_check_tensors(codes, scales), stream, _mx_dequantize, codes, scales, dtype)
 
 
 def _mx_dequantize(handle, codes, scales, dtype):
