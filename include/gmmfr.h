@@ -376,12 +376,12 @@ typedef struct {
  * SwiGLU and weights (e,n,k) one expert's weights at most 2 GiB; every base
  * pointer 16-byte aligned.  Device data are not validated: a broken groupList
  * is clamped as in gmm_finalize_routing.
- * Stage 1: validate (host only) and report the workspace size. */
+ * Stage 1: validate (host only) and report the workspace size, which is 0. */
 int gmm_grouped_matmul_workspace(const gmmgm_args* args, size_t* workspace_bytes);
 
 /* Stage 2: validate again and enqueue on `stream` (hipStream_t; NULL = null
- * stream).  Returns GMMFR_OK, a validation status, GMMFR_ERR_WORKSPACE or
- * GMMFR_ERR_HIP.  y must not overlap an input. */
+ * stream).  `workspace` is not used and may be NULL.  Returns GMMFR_OK, a
+ * validation status or GMMFR_ERR_HIP.  y must not overlap an input. */
 int gmm_grouped_matmul(const gmmgm_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*

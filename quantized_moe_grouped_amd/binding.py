@@ -499,18 +499,11 @@ def _on(dev, stream, call, *args):
             return call(ts.cuda_stream, *args)
 
 
-def _enqueue(name: str, raw: bytes, workspace, dev, handle) -> None:
-    """Stage 2; where it wants a workspace and none is given, stage 1 sizes one first."""
-    L = lib()
+def _enqueue(name: str, raw: bytes, workspace, handle) -> None:
+    """Stage 2.  These calls want no workspace (stage 1 says 0 bytes); one that
+    is given is passed on."""
     ptr, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = getattr(L, name)(raw, ptr, size, handle)
-    if st == ERR_WORKSPACE and workspace is None:
-        import torch
-        need = ctypes.c_size_t(0)
-        st = getattr(L, name + "_workspace")(raw, need)
-        if st == OK:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
-            st = getattr(L, name)(raw, workspace.data_ptr(), need.value, handle)
+    st = getattr(lib(), name)(raw, ptr, size, handle)
     if st != OK:
         raise GmmfrError(st, name)
 
@@ -541,7 +534,7 @@ def _grouped_matmul(handle, x, w, group_list, x_scale, w_scale, out, out_dtype, 
         out = torch.empty((x.shape[0], columns), dtype=dtype, device=x.device)
     tuning, tail = _packed_tuning(tuning_config)
     raw = _gm_bytes(x, w, group_list, out, x_scale, w_scale, group_list_type, transpose_w, activation, tail)
-    _enqueue("gmm_grouped_matmul", raw, workspace, x.device, handle)
+    _enqueue("gmm_grouped_matmul", raw, workspace, handle)
     del tuning  # the host array lives until the call has read it
     return out
 
@@ -569,7 +562,7 @@ def _grouped_matmul_wgrad(handle, x, dy, group_list, out, out_dtype, accumulate,
                           device=x.device)
     tuning, tail = _packed_tuning(tuning_config)
     raw = _gw_bytes(x, dy, group_list, out, group_list_type, accumulate, tail)
-    _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, x.device, handle)
+    _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
     del tuning
     return out
 

@@ -789,8 +789,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     }
   };
-  // Returns whether every lane issued every store (a tile without a rest).
-  auto epilogue = [&](const Tile& c) -> bool {
+  auto epilogue = [&](const Tile& c) {
     int lane = threadIdx.x & 63;  // opaque, as in set_sources
     asm volatile("" : "+v"(lane));
     // sum_at's asm reads products' results: past the 18 wait states that the
@@ -817,7 +816,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         }
       }
     }
-    return c.valid == BM && c.n0 + (GLU ? BN / 2 : BN) <= F && !(WGRAD && p.accumulate);
   };
   auto clear = [&]() {
 #pragma unroll
