@@ -309,7 +309,12 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   __shared__ __attribute__((aligned(16))) uint32_t s_sc2[MX && KWAVES ? STAGES * SROWS : 1];
   // else: the scales of two steps, SB words a row
   __shared__ __attribute__((aligned(16))) uint32_t s_step[MX && !KWAVES ? 2 * SROWS * SB : 1];
-  __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? 2 * FM * FN * 4 * 64 : 1];
+  // KWAVES: the sums of one wave
+  __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? FM * FN * 4 * 64 : 1];
+  static_assert(NT > 256 || BM > 128 ||
+                    sizeof(sX) + sizeof(sW) + sizeof(s_sc) + sizeof(s_sc2) + sizeof(s_step) + sizeof(s_sum) +
+                            (2 * kMaxExperts + 1) * 4 <= 80 * 1024,
+                "two workgroups a CU");
   extern __shared__ __attribute__((aligned(16))) int32_t s_dyn[];
   int32_t* s_ends = s_dyn;
   int32_t* s_pre = s_dyn + p.e;
@@ -881,31 +886,41 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         multiply(xf, wf, std::integral_constant<int, 0>{}, nothing);
         st = st + 1 == STAGES ? 0 : st + 1;
       }
-      // the waves' sums meet in the first wave: (0 + 2) + (1 + 3)
-      static_assert(!KWAVES || NWAVES == 4, "two rounds");
+      // The waves' sums meet in the first wave: (0 + 2) + (1 + 3).  Wave 3 gives
+      // its own in the stage read last, free until the next copies: with 8 KB
+      // of LDS more instead of 16 two workgroups fit a CU whatever the number
+      // of experts, whose table takes up to 8 KB (1024 experts of 2048 x 1024,
+      // 4 rows each: bf16 725 -> 682 us, FP4 407 -> 252; 256 of 2048 x 7168,
+      // skewed, FP8: 479.6 -> 481.3).
+      static_assert(!KWAVES || (NWAVES == 4 && W_BYTES >= FM * FN * 4 * 64 * 16), "two rounds, a wave's sums within a stage");
       constexpr int Q = FM * FN * 4;
+      v4f* in_stage = (v4f*)(sW + (st == 0 ? STAGES - 1 : st - 1) * W_BYTES);
+      auto give = [&](v4f* to) {
 #pragma unroll
-      for (int round = 0; round < 2; ++round) {
-        const int half = round == 0 ? 2 : 1;  // waves half .. 2 half - 1 give, 0 .. half - 1 take
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const v16f& a = acc[q / 4 / FN][q / 4 % FN];
-            s_sum[((wave - half) * Q + q) * 64 + lane] =
-                v4f{a[q % 4 * 4], a[q % 4 * 4 + 1], a[q % 4 * 4 + 2], a[q % 4 * 4 + 3]};
-          }
+        for (int q = 0; q < Q; ++q) {
+          const v16f& a = acc[q / 4 / FN][q / 4 % FN];
+          to[q * 64 + lane] = v4f{a[q % 4 * 4], a[q % 4 * 4 + 1], a[q % 4 * 4 + 2], a[q % 4 * 4 + 3]};
         }
-        lds_barrier();
-        if (wave < half) {
+      };
+      auto take = [&](const v4f* from) {
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const v4f o = s_sum[(wave * Q + q) * 64 + lane];
+        for (int q = 0; q < Q; ++q) {
+          const v4f o = from[q * 64 + lane];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + r] += o[r];
-          }
+          for (int r = 0; r < 4; ++r) acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + r] += o[r];
         }
-        if (round == 0) lds_barrier();  // taken, before wave 1 gives in the same place
+      };
+      lds_barrier();  // all have read that stage
+      if (wave == 2) give(s_sum);
+      if (wave == 3) give(in_stage);
+      lds_barrier();
+      if (wave == 0) take(s_sum);
+      if (wave == 1) {
+        take(in_stage);
+        give(in_stage);
       }
+      lds_barrier();
+      if (wave == 0) take(in_stage);
       if (wave == 0) epilogue(c);
       const int t = tile_at(++jc);
       if (t < 0) break;
