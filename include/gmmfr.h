@@ -362,10 +362,10 @@ typedef struct {
   int64_t group_list_type;  /* 0 or 1                                                         */
   int32_t transpose_w;      /* 0 or 1; must be 1 for microscaled operands                     */
   int32_t activation;       /* gmmgm_activation                                               */
-  /* host array, may be NULL: [0] expected rows per expert (0: m over the smaller
-   * of e and m), which the tile follows; [1] forces the tile height, 32, 128 or
-   * 256 (0: chosen); [2] caps the workgroups of the persistent launch (0: no
-   * cap).  Results do not depend on [2], and on [0] and [1] only in the order
+  /* host array, may be NULL: [0] expected rows of an expert that has any (0: m
+   * over the smaller of e and m), which the tile follows, with the number of
+   * such experts that m allows; [1] forces the tile height, 32, 128 or 256 (0:
+   * chosen); [2] caps the workgroups of the persistent launch (0: no cap).  Results do not depend on [2], and on [0] and [1] only in the order
    * of the fp32 additions. */
   const int64_t* tuning_config;
   int64_t tuning_config_len;
@@ -383,6 +383,14 @@ int gmm_grouped_matmul_workspace(const gmmgm_args* args, size_t* workspace_bytes
  * stream).  `workspace` is not used and may be NULL.  Returns GMMFR_OK, a
  * validation status or GMMFR_ERR_HIP.  y must not overlap an input. */
 int gmm_grouped_matmul(const gmmgm_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Description of the plan stage 2 would use for `args` (host only). */
+typedef struct {
+  int32_t tile_m, tile_n;   /* rows and weight columns of a tile               */
+  int32_t grid;             /* workgroups of the launch (0 without rows)       */
+} gmmgm_plan_info;
+
+int gmm_grouped_matmul_plan(const gmmgm_args* args, gmmgm_plan_info* info);
 
 /*
  * Gradient of the weights of a grouped product: for every expert

@@ -28,7 +28,7 @@ EXPORTED = ("gmm_finalize_routing_workspace", "gmm_finalize_routing", "gmm_final
             "gmm_finalize_routing_plan", "gmmfr_status_string", "gmm_quant_permute_workspace",
             "gmm_quant_permute", "gmm_quant_permute_profiled", "gmm_finalize_routing_noalloc",
             "gmm_grouped_matmul_workspace", "gmm_grouped_matmul", "gmm_grouped_matmul_wgrad_workspace",
-            "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize")
+            "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize", "gmm_grouped_matmul_plan")
 ACTIVATION = {None: 0, "none": 0, "swiglu": 1}
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GMMFR_NOALLOC_SCRATCH_BYTES
 
@@ -72,6 +72,10 @@ class GmArgs(ctypes.Structure):
         ("group_list_type", ctypes.c_int64), ("transpose_w", ctypes.c_int32), ("activation", ctypes.c_int32),
         ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
     ]
+
+
+class GmPlanInfo(ctypes.Structure):
+    _fields_ = [("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32), ("grid", ctypes.c_int32)]
 
 
 class GwArgs(ctypes.Structure):
@@ -128,6 +132,8 @@ def lib():
             getattr(L, name + "_workspace").restype = ctypes.c_int
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
+        L.gmm_grouped_matmul_plan.argtypes = [ctypes.c_void_p, ctypes.POINTER(GmPlanInfo)]
+        L.gmm_grouped_matmul_plan.restype = ctypes.c_int
         for name in ("gmm_mx_quantize", "gmm_mx_dequantize"):
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
@@ -452,6 +458,15 @@ def make_gm_args(x, w, group_list, y, *, x_scale=None, w_scale=None, group_list_
     tuning, tail = _packed_tuning(tuning_config)
     raw = _gm_bytes(x, w, group_list, y, x_scale, w_scale, group_list_type, transpose_w, activation, tail)
     return GmArgs.from_buffer_copy(raw), (x, w, group_list, y, x_scale, w_scale, tuning)
+
+
+def gm_plan(args: GmArgs) -> dict:
+    """The plan gmm_grouped_matmul takes for these arguments (host only)."""
+    info = GmPlanInfo()
+    st = lib().gmm_grouped_matmul_plan(ctypes.byref(args), ctypes.byref(info))
+    if st != OK:
+        raise GmmfrError(st, "gmm_grouped_matmul_plan")
+    return {"tile_m": info.tile_m, "tile_n": info.tile_n, "grid": info.grid}
 
 
 def make_gw_args(x, dy, group_list, dw, *, group_list_type: int = 0, accumulate: bool = False,

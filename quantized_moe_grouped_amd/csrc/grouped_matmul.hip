@@ -1189,11 +1189,27 @@ int product_plan(const gmmgm_args* a, Plan* pl) {
   // to three quarters of a tile, then half a tile of each cut short (bf16, 64
   // experts of 188 rows, 2048 x 7168: 606 us with half a tile cut always, 501 so;
   // FP8 315 and 258, and with much skewed groups 299 and 302).
-  const int64_t parts = e < m ? e : m, avg = rows > 0 ? rows : m / (parts > 0 ? parts : 1);
-  const int64_t middle = parts * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
+  // With expected rows: as many experts as m has of them, each in whole tiles of
+  // that many (2048 x 7168 bf16 (e,k,n), us under 128-row and 256-row tiles; the
+  // one taken without them, and with):
+  //   8 of 256 experts, 1024 rows each of m = 8192   298, 236   first, second
+  //   32 of 256, 256 rows each of m = 8192           335, 272   first, second
+  //   32 experts, 40 rows each of m = 32768          192, 216   second, first
+  //   32 experts, 150 rows each of m = 32768         265, 245   second, second
+  const int64_t parts = e < m ? e : m;
+  if (rows > m) rows = m;
+  int64_t avg = m / (parts > 0 ? parts : 1), busy = parts;
+  if (rows > 0) {
+    avg = rows;
+    if (ceil_div(m, rows) < busy) busy = ceil_div(m, rows);
+  }
+  const int64_t middle = busy * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
   const bool narrow = avg <= 16 ? !pl->col || middle <= 256
                                 : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256));
-  auto along = [&](int64_t t) { return 4 * m <= 3 * t * parts ? 2 * parts : 2 * m / t + parts; };
+  auto along = [&](int64_t t) {
+    if (rows > 0) return 2 * busy * ceil_div(rows, t);
+    return 4 * m <= 3 * t * busy ? 2 * busy : 2 * m / t + busy;
+  };
   pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
                     : (narrow ? kSmall : larger_kind(along(256), along(128), n, mx));
   const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
@@ -1310,6 +1326,17 @@ int wgrad_run(const gmmgw_args* a, void* stream) {
 extern "C" {
 
 using namespace gmmgm;
+
+int gmm_grouped_matmul_plan(const gmmgm_args* args, gmmgm_plan_info* info) {
+  Plan pl;
+  const int st = product_plan(args, &pl);
+  if (st != GMMFR_OK) return st;
+  if (!info) return GMMFR_ERR_NULLPTR;
+  info->tile_m = kTileM[pl.kind];
+  info->tile_n = kTileN[pl.kind];
+  info->grid = pl.p.m == 0 ? 0 : pl.grid;
+  return GMMFR_OK;
+}
 
 int gmm_grouped_matmul_workspace(const gmmgm_args* args, size_t* workspace_bytes) {
   Plan pl;
