@@ -42,7 +42,7 @@ def parse():
     ap.add_argument("--config", default="prefill",
                     choices=["tiny", "decode", "skewed", "prefill", "int4", "mxa8w4", "fp8", "dispatch", "layer"])
     ap.add_argument("--combine", default="auto", choices=["auto", "atomic", "ordered"])
-    ap.add_argument("--quant", default="int8", choices=["int8", "fp8", "mx"],
+    ap.add_argument("--quant", default="int8", choices=["int8", "fp8", "mx", "mx4"],
                     help="dispatch workload: x1 encoding of the producer step")
     ap.add_argument("--deterministic", action="store_true")
     ap.add_argument("--seed", type=int, default=0)
@@ -215,10 +215,12 @@ def dispatch_bytes(rp):
     map and writes x1 and pertokenScale; the step adds the router outputs read
     and rowIndex, logit and groupList written."""
     m = rp.T * rp.K
-    sbytes = m * (rp.k // 32) if getattr(rp, "mode", "int8") == "mx" else m * 4  # pertokenScale written
-    kern = rp.T * rp.k * 2 + m * 4 + m * rp.k + sbytes
+    mode = getattr(rp, "mode", "int8")
+    sbytes = m * (rp.k // 32) if mode in ("mx", "mx4") else m * 4  # pertokenScale written
+    cbytes = m * rp.k // (2 if mode == "mx4" else 1)  # x1 written
+    kern = rp.T * rp.k * 2 + m * 4 + cbytes + sbytes
     step = (rp.T * rp.k * 2 + m * rp.expert_ids.itemsize + (0 if rp.topk_weights is None else m * 4)
-            + m * rp.k + sbytes + (0 if rp.topk_weights is None else m * 4) + m * 8 + rp.e * 8)
+            + cbytes + sbytes + (0 if rp.topk_weights is None else m * 4) + m * 8 + rp.e * 8)
     return step, kern
 
 
@@ -238,8 +240,11 @@ def bench_dispatch(args):
     ids = torch.from_numpy(rp.expert_ids).to(dev)
     w = torch.from_numpy(rp.topk_weights).to(dev)
     m = rp.T * rp.K
-    x1 = torch.empty((m, rp.k), dtype=torch.int8 if rp.mode == "int8" else torch.float8_e4m3fn, device=dev)
-    if rp.mode == "mx":
+    if rp.mode == "mx4":
+        x1 = torch.empty((m, rp.k // 2), dtype=torch.float4_e2m1fn_x2, device=dev)
+    else:
+        x1 = torch.empty((m, rp.k), dtype=torch.int8 if rp.mode == "int8" else torch.float8_e4m3fn, device=dev)
+    if rp.mode in ("mx", "mx4"):
         pts = torch.empty((m, rp.k // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
     else:
         pts = torch.empty(m, dtype=torch.float32, device=dev)
@@ -279,7 +284,7 @@ def bench_dispatch(args):
         "metric": "GB/s (and % of HBM roofline) of per-token int8 quantisation + routing permute at 1 GPU",
         "value": round(gbs, 1), "unit": "GB/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
         "ms_per_step": round(ms_step, 5), "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
-        "dtype": {"int8": "bf16->int8", "fp8": "bf16->fp8", "mx": "bf16->fp8+e8m0"}[rp.mode],
+        "dtype": {"int8": "bf16->int8", "fp8": "bf16->fp8", "mx": "bf16->fp8+e8m0", "mx4": "bf16->fp4+e8m0"}[rp.mode],
         "data": "synthetic (seeded generator; bf16 hidden states, top-8 of 32 router choices with softmax weights)",
         "config": {"workload": "dispatch" if rp.mode == "int8" else "dispatch-" + rp.mode, "tokens": rp.T,
                    "k": rp.k, "top_k": rp.K, "e": rp.e, "m": m, "quant": rp.mode,

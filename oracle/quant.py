@@ -41,7 +41,9 @@ giving only the mode names and the multiply by an inverse scale):
                   largest E4M3 exponent), clamped to [-127, 127] (-127 for an
                   all-zero block), E8M0 code s + 127, element code
                   E4M3(clamp(x * 2^-s, -448, 448)).
-E4M3(v) rounds to the nearest E4M3 value, ties to the even code.
+  mx4 (per 32 k): the same for FP4 E2M1, whose largest exponent is 2: codes of
+                  E2M1(clamp(x * 2^-s, -6, 6)), two per byte.
+E4M3(v) and E2M1(v) round to the nearest value, ties to the even code.
 """
 from __future__ import annotations
 
@@ -125,6 +127,28 @@ def quantize_mx(hidden_bits):
     return e4m3_encode(v).reshape(T, k), (s + 127).astype(np.uint8)
 
 
+def quantize_mx4(hidden_bits):
+    """MX FP4 per 32 values: (bytes uint8 (T,k/2), the lower nibble first, E8M0
+    codes uint8 (T, k/32)).  As quantize_mx with the largest E2M1 exponent, 2,
+    values saturated at 6."""
+    x = bf16_to_f32(hidden_bits).astype(np.float64)
+    T, k = x.shape
+    if k % 32:
+        raise ValueError("k must be a multiple of 32")
+    xb = x.reshape(T, k // 32, 32)
+    amax = np.abs(xb).max(axis=2, initial=0.0)
+    if not np.isfinite(amax).all():
+        raise ValueError("hidden values must be finite")
+    s = np.clip(np.where(amax > 0, np.frexp(amax)[1] - 1 - 2, -127), -127, 127)
+    v = xb * np.exp2(-s)[:, :, None]
+    a = np.minimum(np.abs(v), 6.0)
+    # codes 0..7 are 0 0.5 1 1.5 2 3 4 6: halves up to 2, whole numbers up to 4,
+    # then steps of 2; ties to the even multiple are ties to the even code
+    code = np.where(a <= 2, np.rint(a * 2), np.where(a <= 4, np.rint(a) + 2, np.rint(a / 2) + 4)).astype(np.uint8)
+    code = (code | (np.signbit(v).astype(np.uint8) << 3)).reshape(T, k)
+    return code[:, 0::2] | (code[:, 1::2] << 4), (s + 127).astype(np.uint8)
+
+
 def permute(expert_ids, e: int, expert_offset: int = 0):
     """Steps 2-3 on the indices: (order of flat entries f, counts (e))."""
     ids = np.asarray(expert_ids).astype(np.int64).reshape(-1)
@@ -137,7 +161,8 @@ def permute(expert_ids, e: int, expert_offset: int = 0):
 
 def run(rp):
     """All four steps.  Returns a dict: x1 (m,k) int8 (FP8 modes: uint8 E4M3
-    codes), pertoken_scale (m) float32 (mx: uint8 E8M0 codes (m, k/32)),
+    codes; mx4: uint8 bytes (m,k/2)), pertoken_scale (m) float32 (mx and mx4:
+    uint8 E8M0 codes (m, k/32)),
     logit (m) or None, row_index (m) int64, group_list (e) int64, and
     ``rows`` = sum(counts); entries at and past ``rows`` are zero here and
     undefined in the operator."""
@@ -153,13 +178,15 @@ def run(rp):
         q, scale = quantize_fp8(rp.hidden)
     elif mode == "mx":
         q, scale = quantize_mx(rp.hidden)
+    elif mode == "mx4":
+        q, scale = quantize_mx4(rp.hidden)
     else:
         raise ValueError(mode)
     order, counts = permute(rp.expert_ids, e, rp.expert_offset)
     m = T * K
     rows = len(order)
     tok = order // K if K > 0 else order
-    x1 = np.zeros((m, k), dtype=q.dtype)
+    x1 = np.zeros((m, q.shape[1]), dtype=q.dtype)
     x1[:rows] = q[tok]
     pts = np.zeros((m,) + scale.shape[1:], dtype=scale.dtype)
     pts[:rows] = scale[tok]

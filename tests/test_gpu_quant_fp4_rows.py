@@ -82,3 +82,20 @@ def test_drawn_fp4_rows(seed):
                          with_weights=bool(rng.random() < 0.8), group_list_type=int(rng.integers(2)),
                          zero_tokens=int(rng.integers(0, 3)), repeat_slots=bool(rng.random() < 0.2))
     _check(rp, torch.int32 if rng.random() < 0.3 else torch.int64)
+
+
+def test_fp4_rows_of_the_dispatch_workload():
+    """16384 tokens, k = 2048, top-8 of 32 experts, against the whole oracle."""
+    rp = W.make_route_config("dispatch", 0)
+    rp.mode = "mx4"
+    ref = Q.run(rp)
+    hidden = torch.from_numpy(rp.hidden.view(np.int16)).cuda().view(torch.bfloat16)
+    got = B.quant_permute(hidden, torch.from_numpy(rp.expert_ids).cuda(), rp.e,
+                          topk_weights=torch.from_numpy(rp.topk_weights).cuda(), group_list_type=rp.group_list_type, mode="mx4")
+    rows = ref["rows"]
+    assert np.array_equal(got["x1"].view(torch.uint8).cpu().numpy()[:rows], ref["x1"][:rows])
+    assert np.array_equal(got["pertoken_scale"].view(torch.uint8).cpu().numpy().reshape(len(ref["x1"]), -1)[:rows],
+                          ref["pertoken_scale"][:rows])
+    assert np.array_equal(got["row_index"].cpu().numpy()[:rows], ref["row_index"][:rows])
+    assert np.array_equal(got["group_list"].cpu().numpy(), ref["group_list"])
+    assert np.array_equal(got["logit"].cpu().numpy()[:rows], ref["logit"][:rows])
