@@ -486,17 +486,21 @@ def _check_tensors(x, *others):
     """The device of x.  No tensor may want a gradient that these calls would
     lose (they record no history), and all live on one GPU, where the kernels
     dereference their pointers."""
-    import torch
-    tensors = [t for t in (x, *others) if t is not None]
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError("these calls record no gradients: detach the tensors, or call them under torch.no_grad() or in "
-                         "a torch.autograd.Function of your own")
-    dev = x.device
+    dev, wanting, elsewhere = x.device, x.requires_grad, None
+    for t in others:
+        if t is not None:
+            wanting = wanting or t.requires_grad
+            if t.device != dev:
+                elsewhere = t.device
+    if wanting:
+        import torch
+        if torch.is_grad_enabled():
+            raise ValueError("these calls record no gradients: detach the tensors, or call them under torch.no_grad() or "
+                             "in a torch.autograd.Function of your own")
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {dev}")
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors must be on one device: {t.device} and {dev}")
+    if elsewhere is not None:
+        raise ValueError(f"tensors must be on one device: {elsewhere} and {dev}")
     return dev
 
 
