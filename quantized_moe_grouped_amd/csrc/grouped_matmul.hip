@@ -32,15 +32,19 @@
 //     bytes.
 //
 // What bounds it (one MI355X; rows over experts):
-//   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.91 ms,
-//     1.06 PFLOP/s.  Matrix cores busy 64% of the cycles at the 1.74 GHz that
-//     the card's power leaves; between them the waits for LDS and barriers.
-//   - weight gradient of the same: 1.11 ms, 45% busy at 1.88 GHz: one
+//   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.90 to 0.95
+//     ms from box to box, 1.02 to 1.06 PFLOP/s.  Matrix cores busy 64% of the
+//     cycles at the 1.74 GHz that the card's power leaves; between them the
+//     waits for LDS and barriers.
+//   - weight gradient of the same: 1.11 ms, 45% busy at 1.92 GHz: one
 //     workgroup a CU (its sums fill the registers), whose 1.9 GB of fp32
-//     results nothing else covers.
-//   - FP4, 131072 x 7168 x 4096 over 32, SwiGLU: 2.05 ms, 3.75 PFLOP/s: a
-//     product is a quarter of the 16-bit one's time, and the copies' share of
-//     the address path, scales included, fills the rest.
+//     results go out ahead of copies that the next tile's first step waits for.
+//   - FP4, 131072 x 7168 x 4096 over 32, SwiGLU: 2.01 to 2.08 ms, 3.7 to 3.8
+//     PFLOP/s, 51% busy at 1.76 GHz: a product is a quarter of the 16-bit one's
+//     time for the same bytes copied and read.
+//   - FP8 with FP4, 30001 x 2112 x 7152 over 64: 0.61 ms, 46% busy; a third of
+//     the rows multiplied do not exist, and reads of 64-byte rows of weights
+//     conflict in 28% of the LDS' active cycles.
 //   - rows whose bytes are no multiple of 128 cost twice the requests to the
 //     L2: fp16, 20011 rows over 64, 2040 columns, 128-row tiles: 1.02 ms with
 //     k = 7160, 0.80 ms with 7168.
@@ -724,6 +728,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       return acc[i][j][r];
     }
   };
+  // An fp32 sum but for FP8 with FP4: there the instruction drops what lies 2^-14
+  // below a 32-value block's largest product (no other takes these types; before
+  // their rounding such outputs are 1.5e-5 of their norm off, FP4 with FP4 5e-8).
   // between(m): what is issued after product m of the slice
   auto multiply = [&](XFrag (&xf)[FM], WFrag (&wf)[FN], auto s_, auto between) {
     constexpr int S = KWAVES ? 0 : decltype(s_)::value * (NS == 4 ? 1 : 2);  // byte of the scale registers
@@ -1100,7 +1107,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // tiles (two a CU) taking 0.6 of a round of 256 large ones, 0.65 with
 // microscaled operands (measured at 32768 x 2048 x 7168 over 32 experts, 16
 // bit: 1.15 against 0.95 ms for the same work; FP4, 12000 x 7168 x 4096 over
-// 64: 8 rounds in 0.41 ms against 5 in 0.34).
+// 64: 8 rounds in 0.41 ms against 5 in 0.34).  Other shapes have other factors:
+// fp16 (e,n,k), 20011 x 7160 x 2040 over 64, falls to the 128-row tiles by it (4
+// rounds against 6), 1011 us, where 256-row ones take 977.
 Kind larger_kind(int64_t large, int64_t middle, int64_t columns, bool mx) {
   const int64_t l = ceil_div(large * ceil_div(columns, 256), 2 * 256), m = ceil_div(middle * ceil_div(columns, 128), 2 * 512);
   return l * 100 <= m * (mx ? 65 : 60) ? kLarge : kMiddle;
