@@ -506,7 +506,11 @@ def _check_tensors(x, *others):
 
 def _on(dev, stream, call, *args):
     """call(raw stream handle, *args) with `dev` current and, where a stream is
-    given, that stream too (so that what the call allocates comes from its pool)."""
+    given, that stream too (so that what the call allocates comes from its pool).
+    Tensors among args are then marked as used on it: freed on return, their
+    memory waits for the kernels before it is handed out again.  (Not on a
+    stream that the caller made outside torch, and may destroy: there the
+    caller keeps them alive.)"""
     import torch
     if stream is None and torch.cuda.current_device() == dev.index:
         return call(torch._C._cuda_getCurrentRawStream(dev.index), *args)
@@ -515,7 +519,12 @@ def _on(dev, stream, call, *args):
         if ts.device != dev:
             raise ValueError(f"the stream is on {ts.device}, the tensors on {dev}")
         with torch.cuda.stream(ts):
-            return call(ts.cuda_stream, *args)
+            result = call(ts.cuda_stream, *args)
+        if not isinstance(ts, torch.cuda.ExternalStream):
+            for t in args:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(ts)
+        return result
 
 
 def _enqueue(name: str, raw: bytes, workspace, handle) -> None:
