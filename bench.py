@@ -294,7 +294,8 @@ def bench_dispatch(args):
         "roofline": {"bound": "hbm", "kernel": "quant_rows_kernel", "achieved": round(kgbs, 1),
                      "peak": PEAK_HBM_GBS, "unit": "GB/s", "frac": round(kgbs / PEAK_HBM_GBS, 4),
                      "launch_ms": round(q_avg, 5), "bytes_per_launch": kern_bytes,
-                     "traffic": traffic_from_profiles("quant_rows_kernel", "dispatch", "quant_rows_kernel", QP_SRC)},
+                     "traffic": (None if rp.mode == "mx4"  # counted with x1 of a byte a value
+                                 else traffic_from_profiles("quant_rows_kernel", "dispatch", "quant_rows_kernel", QP_SRC))},
         "cpu_baseline": None,
     }
     if not args.no_cpu_baseline:
