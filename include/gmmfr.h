@@ -365,8 +365,9 @@ typedef struct {
   /* host array, may be NULL: [0] expected rows of an expert that has any (0: m
    * over the smaller of e and m), which the tile follows, with the number of
    * such experts that m allows; [1] forces the tile height, 32, 128 or 256 (0:
-   * chosen); [2] caps the workgroups of the persistent launch (0: no cap).  Results do not depend on [2], and on [0] and [1] only in the order
-   * of the fp32 additions. */
+   * chosen); [2] caps the workgroups of the persistent launch (0: no cap).
+   * Results do not depend on [2], and on [0] and [1] only in the order of the
+   * fp32 additions. */
   const int64_t* tuning_config;
   int64_t tuning_config_len;
 } gmmgm_args;

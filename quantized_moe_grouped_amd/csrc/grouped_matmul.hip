@@ -222,24 +222,23 @@ __device__ void group_table(const Params& p, int bm, int32_t* s_ends, int32_t* s
 __device__ __forceinline__ float swiglu(float u, float v) {
   return u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f)) * v;
 }
-// The same for any u, with h = exp(-|u| / 2): u / (1 + h h) * v for u >= 0,
-// u h / (1 + h h) * v * h below.  h stays normal down to u = -174, past which
-// less than 2^-115 is left of any v.
+// The same below that, with h = exp(u / 2): u h * v * h (1 + h h is 1).  h stays
+// normal down to u = -174, past which less than 2^-115 is left of any v.
 __device__ __forceinline__ float swiglu_far(float u, float v) {
-  const float h = __builtin_amdgcn_exp2f(__builtin_fabsf(u) * -0.72134752f);
-  const float below = u < 0 ? h : 1.0f;
-  return u * below * __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f)) * v * below;
+  const float h = __builtin_amdgcn_exp2f(u * 0.72134752f);
+  return u * h * v * h;
 }
-// For a lane's 16 values.  Gates below -87 are rare, and the far form for all
-// would cost 1.3% (FP4, 131072 x 7168 x 4096 over 32 experts: 2034 -> 2060 us;
-// the test of the gates 0.5%): the wave takes it where one of its gates needs it.
+// For a lane's 16 values.  Gates below -87 are rare: both forms, and a choice for
+// each value by its own gate alone, only where a lane of the wave has one (a form
+// right for all gates, taken for all: 1.3%, FP4, 131072 x 7168 x 4096 over 32
+// experts, 2034 -> 2060 us; the test of the gates 0.5%).
 __device__ __forceinline__ void swiglu16(const float (&u)[16], const float (&v)[16], float (&o)[16]) {
   uint32_t least = 0;  // the most negative gate has the largest bits
 #pragma unroll
   for (int r = 0; r < 16; ++r) least = max(least, __float_as_uint(u[r]));
   if (__any(least > __float_as_uint(-87.0f))) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[r] = swiglu_far(u[r], v[r]);
+    for (int r = 0; r < 16; ++r) o[r] = u[r] < -87.0f ? swiglu_far(u[r], v[r]) : swiglu(u[r], v[r]);
   } else {
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[r] = swiglu(u[r], v[r]);

@@ -68,3 +68,23 @@ def test_swiglu_of_microscaled_gates(height):
     both = torch.cat([gates.double()[:, None].expand(-1, f), torch.full((len(gates), f), 2.0 ** 90, dtype=torch.float64)], 1)
     want, err = R.swiglu(both, torch.zeros_like(both))
     R.assert_within(y, want, err + R.half_step(want.abs() + err, F32), "swiglu")
+
+
+@pytest.mark.parametrize("height", [32, 128, 256])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_a_row_does_not_depend_on_its_neighbours_gates(height, out_dtype):
+    """Rows beside ones with far gates, bit for bit as without them."""
+    gen = torch.Generator().manual_seed(33)
+    m, k, f = 96, 64, 64
+    x = torch.randn((m, k), generator=gen).to(BF16)
+    w = torch.randn((1, k, 2 * f), generator=gen).to(BF16)
+    w[0, 0, :f] = 1
+    x[:, 0] = 0
+    gl = torch.tensor([m]).cuda()
+
+    def call(x):
+        return B.grouped_matmul(x.cuda(), w.cuda(), gl, activation="swiglu", out_dtype=out_dtype, tuning_config=[0, height]).cpu()
+    far = torch.arange(m) % 7 == 3
+    beside = x.clone()
+    beside[far, 0] = -200.0
+    assert torch.equal(call(x)[~far], call(beside)[~far])
