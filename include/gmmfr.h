@@ -417,6 +417,77 @@ int gmm_grouped_matmul_wgrad_workspace(const gmmgw_args* args, size_t* workspace
 int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The gated feed-forward block of the experts (e = 1: of a dense layer, or of a
+ * shared expert), in training or in serving:
+ *
+ *   u = columns 0 .. f-1 and v = columns f .. 2f-1 of the product x w[g]
+ *   h[i][j] = a(u) * v,   a(u) = u * s(z),   s(z) = 1 / (1 + exp(-z))
+ *   SWIGLU: z = u;   GEGLU (gelu in its tanh form): z = sqrt(8/pi) (u + 0.044715 u^3)
+ *
+ * in fp32, rounded once to h's type.  u and v themselves can be kept for the
+ * backward pass, side by side as (m, 2f): in x's type, or as FP8 codes with one
+ * E8M0 scale per 32 columns, the layout and the rules of gmm_mx_quantize on the
+ * fp32 values (f % 32 == 0).  A value is rounded once either way; h is made of
+ * the values before that.
+ * Rows behind the last group are not read, and theirs of h and of what is kept
+ * are left as they are.
+ */
+typedef enum { GMMGF_ACT_SWIGLU = 1, GMMGF_ACT_GEGLU = 2 } gmmgf_activation;
+
+typedef struct {
+  gmmfr_tensor x;           /* BFLOAT16 or FLOAT16 (m,k)                             required */
+  gmmfr_tensor w;           /* x's type (e,k,2f), or (e,2f,k) with transpose_w = 1   required */
+  gmmfr_tensor group_list;  /* INT64 (e); type 0 cumulative ends, type 1 counts      required */
+  gmmfr_tensor h;           /* out x's type (m,f)                                    required */
+  gmmfr_tensor kept;        /* out (m,2f): x's type or FLOAT8_E4M3FN                 optional */
+  gmmfr_tensor kept_scale;  /* out FLOAT8_E8M0 (m,2f/64,2)          given iff kept is FLOAT8  */
+  int64_t group_list_type;  /* 0 or 1                                                         */
+  int32_t transpose_w;      /* 0 or 1                                                         */
+  int32_t activation;       /* gmmgf_activation                                               */
+  const int64_t* tuning_config; /* as gmm_grouped_matmul's */
+  int64_t tuning_config_len;
+} gmmgf_args;
+
+/* Limits and stages: those of gmm_grouped_matmul's 16-bit operands with SwiGLU
+ * (n = 2f: f % 8 == 0).  Outputs must not overlap each other or an input. */
+int gmm_gated_matmul_workspace(const gmmgf_args* args, size_t* workspace_bytes);
+int gmm_gated_matmul(const gmmgf_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its way back, from dy, the gradient behind the block's last projection (h
+ * times weights (e,f,d)), to the gradients of u and v, and h again:
+ *
+ *   dh[i][j] = sum_q dy[i][q] * w[g][j][q]
+ *   du = dh * v * a'(u),  dv = dh * a(u),  h = a(u) * v
+ *
+ * with u and v as they were kept; a'(u) = s (1 + u z'(u) (1 - s)).  All in fp32,
+ * rounded once.  d = (du | dv) is what the gradients of x (gmm_grouped_matmul
+ * with the weights transposed) and of w (gmm_grouped_matmul_wgrad) are made of,
+ * h what the last projection's weight gradient is.  (h of values kept in FP8
+ * differs from the forward pass's by their rounding, as the gradients do.)
+ * Rows behind the last group are not read, and theirs of d and h are left.
+ */
+typedef struct {
+  gmmfr_tensor dy;          /* BFLOAT16 or FLOAT16 (m,d)                             required */
+  gmmfr_tensor w;           /* dy's type: the last projection's weights, (e,f,d) with
+                             * transpose_w = 1, (e,d,f) with transpose_w = 0         required */
+  gmmfr_tensor group_list;  /* INT64 (e)                                             required */
+  gmmfr_tensor kept;        /* (m,2f): dy's type or FLOAT8_E4M3FN                    required */
+  gmmfr_tensor kept_scale;  /* FLOAT8_E8M0 (m,2f/64,2)              given iff kept is FLOAT8  */
+  gmmfr_tensor d;           /* out dy's type (m,2f)                                  required */
+  gmmfr_tensor h;           /* out dy's type (m,f)                                   optional */
+  int64_t group_list_type;
+  int32_t transpose_w;
+  int32_t activation;       /* gmmgf_activation */
+  const int64_t* tuning_config;
+  int64_t tuning_config_len;
+} gmmgb_args;
+
+/* Limits and stages as gmm_gated_matmul's, with d in k's place. */
+int gmm_gated_matmul_backward_workspace(const gmmgb_args* args, size_t* workspace_bytes);
+int gmm_gated_matmul_backward(const gmmgb_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Microscaled quantisation (OCP MX v1.0) of 16- or 32-bit values, in blocks of
  * 32 along k: shared exponent s = floor(log2(block amax)) - 2 for FP4 E2M1 or
  * - 8 for FP8 E4M3, clamped to [-127, 127] (-127 for an all-zero block), E8M0

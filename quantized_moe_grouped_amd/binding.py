@@ -28,8 +28,11 @@ EXPORTED = ("gmm_finalize_routing_workspace", "gmm_finalize_routing", "gmm_final
             "gmm_finalize_routing_plan", "gmmfr_status_string", "gmm_quant_permute_workspace",
             "gmm_quant_permute", "gmm_quant_permute_profiled", "gmm_finalize_routing_noalloc",
             "gmm_grouped_matmul_workspace", "gmm_grouped_matmul", "gmm_grouped_matmul_wgrad_workspace",
-            "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize", "gmm_grouped_matmul_plan")
+            "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize", "gmm_grouped_matmul_plan",
+            "gmm_gated_matmul_workspace", "gmm_gated_matmul", "gmm_gated_matmul_backward_workspace",
+            "gmm_gated_matmul_backward")
 ACTIVATION = {None: 0, "none": 0, "swiglu": 1}
+GATE = {"swiglu": 1, "geglu": 2}  # of the gated block
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GMMFR_NOALLOC_SCRATCH_BYTES
 
 
@@ -86,6 +89,23 @@ class GwArgs(ctypes.Structure):
     ]
 
 
+class GfArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", Tensor), ("w", Tensor), ("group_list", Tensor), ("h", Tensor), ("kept", Tensor), ("kept_scale", Tensor),
+        ("group_list_type", ctypes.c_int64), ("transpose_w", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
+    ]
+
+
+class GbArgs(ctypes.Structure):
+    _fields_ = [
+        ("dy", Tensor), ("w", Tensor), ("group_list", Tensor), ("kept", Tensor), ("kept_scale", Tensor), ("d", Tensor),
+        ("h", Tensor), ("group_list_type", ctypes.c_int64), ("transpose_w", ctypes.c_int32),
+        ("activation", ctypes.c_int32), ("tuning_config", ctypes.POINTER(ctypes.c_int64)),
+        ("tuning_config_len", ctypes.c_int64),
+    ]
+
+
 class MqArgs(ctypes.Structure):
     _fields_ = [("x", Tensor), ("codes", Tensor), ("scales", Tensor), ("transpose", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
@@ -127,7 +147,7 @@ def lib():
                                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
         L.gmm_quant_permute_profiled.restype = ctypes.c_int
         # arguments of these as void*: a struct by reference, or its bytes
-        for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad"):
+        for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad", "gmm_gated_matmul", "gmm_gated_matmul_backward"):
             getattr(L, name + "_workspace").argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]
             getattr(L, name + "_workspace").restype = ctypes.c_int
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
@@ -451,6 +471,16 @@ def _mq_bytes(x, codes, scales, transpose) -> bytes:
     return b"".join((_packed(x), _packed(codes), _packed(scales), _pack_ii(bool(transpose), 0)))
 
 
+def _gf_bytes(x, w, group_list, h, kept, kept_scale, group_list_type, transpose_w, activation, tail) -> bytes:
+    return b"".join((_packed(x), _packed(w), _packed(group_list), _packed(h), _packed(kept), _packed(kept_scale),
+                     _pack_qii(group_list_type, bool(transpose_w), GATE[activation]), tail))
+
+
+def _gb_bytes(dy, w, group_list, kept, kept_scale, d, h, group_list_type, transpose_w, activation, tail) -> bytes:
+    return b"".join((_packed(dy), _packed(w), _packed(group_list), _packed(kept), _packed(kept_scale), _packed(d),
+                     _packed(h), _pack_qii(group_list_type, bool(transpose_w), GATE[activation]), tail))
+
+
 def make_gm_args(x, w, group_list, y, *, x_scale=None, w_scale=None, group_list_type: int = 0,
                  transpose_w: bool = False, activation: Optional[str] = None,
                  tuning_config: Optional[Sequence[int]] = None):
@@ -475,6 +505,22 @@ def make_gw_args(x, dy, group_list, dw, *, group_list_type: int = 0, accumulate:
     tuning, tail = _packed_tuning(tuning_config)
     raw = _gw_bytes(x, dy, group_list, dw, group_list_type, accumulate, tail)
     return GwArgs.from_buffer_copy(raw), (x, dy, group_list, dw, tuning)
+
+
+def make_gf_args(x, w, group_list, h, *, kept=None, kept_scale=None, group_list_type: int = 0,
+                 transpose_w: bool = False, activation: str = "swiglu", tuning_config: Optional[Sequence[int]] = None):
+    """C arguments of gmm_gated_matmul.  Returns (args, keepalive)."""
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gf_bytes(x, w, group_list, h, kept, kept_scale, group_list_type, transpose_w, activation, tail)
+    return GfArgs.from_buffer_copy(raw), (x, w, group_list, h, kept, kept_scale, tuning)
+
+
+def make_gb_args(dy, w, group_list, kept, d, *, kept_scale=None, h=None, group_list_type: int = 0,
+                 transpose_w: bool = True, activation: str = "swiglu", tuning_config: Optional[Sequence[int]] = None):
+    """C arguments of gmm_gated_matmul_backward.  Returns (args, keepalive)."""
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gb_bytes(dy, w, group_list, kept, kept_scale, d, h, group_list_type, transpose_w, activation, tail)
+    return GbArgs.from_buffer_copy(raw), (dy, w, group_list, kept, kept_scale, d, h, tuning)
 
 
 def make_mq_args(x, codes, scales, *, transpose: bool = False):
@@ -593,6 +639,87 @@ def _grouped_matmul_wgrad(handle, x, dy, group_list, out, out_dtype, accumulate,
     _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
     del tuning
     return out
+
+
+def _check_gate(activation):
+    if activation not in GATE:
+        raise ValueError(f"unknown activation {activation!r}: one of {', '.join(GATE)}")
+
+
+def gated_matmul(x, w, group_list, *, activation: str = "swiglu", keep: Optional[str] = None, out=None, kept=None,
+                 kept_scale=None, group_list_type: int = 0, transpose_w: bool = False,
+                 tuning_config: Optional[Sequence[int]] = None, workspace=None, stream=None):
+    """The gated feed-forward block of every expert (or, with one group, of a
+    dense layer): act(x w[..., :f]) * (x w[..., f:]), act silu ("swiglu") or
+    gelu in its tanh form ("geglu").  16-bit x (m,k) and w (e,k,2f), or (e,2f,k)
+    with transpose_w.  keep: the two projections for gated_matmul_backward, in
+    x's type ("full") or in FP8 with one scale per 32 columns ("fp8", as
+    mx_quantize makes them; f % 32 == 0), or not (None).  Returns (h, kept,
+    kept_scale): h (m,f) in x's type, kept (m,2f), kept_scale (m,2f/64,2), the
+    last two None where there are none; `out`, `kept` and `kept_scale` are
+    written to where they are given.  Rows behind the last group are left as
+    they are.  Records no history: tensors that want a gradient are refused."""
+    _check_gate(activation)
+    if keep not in (None, "full", "fp8"):
+        raise ValueError(f"unknown keep {keep!r}: None, 'full' or 'fp8'")
+    if (kept is not None and keep is None) or (kept_scale is not None and keep != "fp8"):
+        raise ValueError("a buffer for what is kept needs keep to say so")
+    dev = _check_tensors(x, w, group_list, out, kept, kept_scale, workspace)
+    return _on(dev, stream, _gated_matmul, x, w, group_list, activation, keep, out, kept, kept_scale, group_list_type,
+               transpose_w, tuning_config, workspace)
+
+
+def _gated_matmul(handle, x, w, group_list, activation, keep, out, kept, kept_scale, group_list_type, transpose_w,
+                  tuning_config, workspace):
+    import torch
+    m, both = x.shape[0], w.shape[1 if transpose_w else 2]
+    if out is None:
+        out = torch.empty((m, both // 2), dtype=x.dtype, device=x.device)
+    if keep is not None and kept is None:
+        kept = torch.empty((m, both), dtype=x.dtype if keep == "full" else torch.float8_e4m3fn, device=x.device)
+    if keep == "fp8" and kept_scale is None:
+        kept_scale = torch.empty((m, both // 64, 2), dtype=torch.float8_e8m0fnu, device=x.device)
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gf_bytes(x, w, group_list, out, kept, kept_scale, group_list_type, transpose_w, activation, tail)
+    _enqueue("gmm_gated_matmul", raw, workspace, handle)
+    del tuning
+    return out, kept, kept_scale
+
+
+def gated_matmul_backward(dy, w, group_list, kept, *, kept_scale=None, activation: str = "swiglu", out=None, h=None,
+                          want_h: bool = True, group_list_type: int = 0, transpose_w: bool = True,
+                          tuning_config: Optional[Sequence[int]] = None, workspace=None, stream=None):
+    """The way back through gated_matmul, from dy (m,d), the gradient behind the
+    block's last projection with weights w (e,f,d), or (e,d,f) with transpose_w
+    = False: dh = dy w^T through the gate to the gradients of the two
+    projections, side by side as (m,2f), and h = act(u) v again (m,f), from what
+    gated_matmul kept.  Returns (d, h), h None without want_h; written to `out`
+    and `h` where they are given.  The other gradients, with w1 the projections'
+    weights (e,k,2f) and x the block's rows:
+    grouped_matmul(d, w1, ..., transpose_w=True) for x,
+    grouped_matmul_wgrad(x, d, ...) for w1, grouped_matmul_wgrad(h, dy, ...) for
+    w.  Rows behind the last group are left as they are.  Records no history."""
+    _check_gate(activation)
+    if h is not None and not want_h:
+        raise ValueError("h is given but not wanted")
+    dev = _check_tensors(dy, w, group_list, kept, kept_scale, out, h, workspace)
+    return _on(dev, stream, _gated_matmul_backward, dy, w, group_list, kept, kept_scale, activation, out, h, want_h,
+               group_list_type, transpose_w, tuning_config, workspace)
+
+
+def _gated_matmul_backward(handle, dy, w, group_list, kept, kept_scale, activation, out, h, want_h, group_list_type,
+                           transpose_w, tuning_config, workspace):
+    import torch
+    m, f = dy.shape[0], w.shape[1 if transpose_w else 2]
+    if out is None:
+        out = torch.empty((m, 2 * f), dtype=dy.dtype, device=dy.device)
+    if want_h and h is None:
+        h = torch.empty((m, f), dtype=dy.dtype, device=dy.device)
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gb_bytes(dy, w, group_list, kept, kept_scale, out, h, group_list_type, transpose_w, activation, tail)
+    _enqueue("gmm_gated_matmul_backward", raw, workspace, handle)
+    del tuning
+    return out, h
 
 
 def mx_quantize(x, *, format: str = "fp4", transpose: bool = False, stream=None):

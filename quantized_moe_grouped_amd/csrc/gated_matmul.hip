@@ -1,0 +1,139 @@
+// The gated feed-forward block of a layer's experts (or, with one group, of a
+// dense layer), for training: both projections, the activation and the product
+// of the two in one kernel, and the way back through all three from behind the
+// block's last projection.
+//
+//   forward:  (u | v) = x W,  h = a(u) v;  (u | v) kept in 16 bits, in FP8, or not
+//   backward: dh = dy Wd^T,  du = dh v a'(u),  dv = dh a(u),  h = a(u) v again
+//
+// Instances of product_kernel (grouped_product.h) whose epilogue works on the
+// fp32 sums in registers (gate.h): neither the projections of the forward pass
+// nor dh of the backward pass goes through memory in between.
+#include "grouped_product.h"
+
+namespace gmmgm {
+
+// What is kept: nothing, x's own type, or FP8 with E8M0 scales; (m, 2 f).
+int kept_plan(const gmmfr_tensor& kept, const gmmfr_tensor& scale, int type, int64_t m, int64_t f, Params* p) {
+  if (!given(kept)) {
+    if (given(scale)) return GMMFR_ERR_NULLPTR;
+    p->keep = kKeepNone;
+  } else if (kept.dtype == GMMFR_DT_FLOAT8_E4M3FN) {
+    if (!given(scale)) return GMMFR_ERR_NULLPTR;
+    if (scale.dtype != GMMFR_DT_FLOAT8_E8M0) return GMMFR_ERR_DTYPE;
+    if (f % 32 != 0 || !shape_is(scale, 3, m, 2 * f / 64, 2)) return GMMFR_ERR_SHAPE;
+    p->keep = kKeepFp8;
+  } else {
+    if (kept.dtype != type) return GMMFR_ERR_DTYPE;
+    if (given(scale)) return GMMFR_ERR_UNSUPPORTED;
+    p->keep = kKeepFull;
+  }
+  if (p->keep != kKeepNone && !shape_is(kept, 2, m, 2 * f)) return GMMFR_ERR_SHAPE;
+  p->kept = kept.data;
+  p->kept_scale = (uint8_t*)scale.data;
+  return aligned({&kept, &scale});
+}
+
+bool in_16_bits(int dtype) { return dtype == GMMFR_DT_BFLOAT16 || dtype == GMMFR_DT_FLOAT16; }
+
+int forward_plan(const gmmgf_args* a, Plan* pl) {
+  if (!a) return GMMFR_ERR_NULLPTR;
+  if (!given(a->x) || !given(a->w) || !given(a->group_list) || !given(a->h)) return GMMFR_ERR_NULLPTR;
+  if (!in_16_bits(a->x.dtype) || a->h.dtype != a->x.dtype) return GMMFR_ERR_DTYPE;
+  if (a->activation != GMMGF_ACT_SWIGLU && a->activation != GMMGF_ACT_GEGLU) return GMMFR_ERR_ATTR;
+  gmmgm_args product = {};
+  product.x = a->x;
+  product.w = a->w;
+  product.group_list = a->group_list;
+  product.y = a->h;
+  product.group_list_type = a->group_list_type;
+  product.transpose_w = a->transpose_w;
+  product.activation = GMMGM_ACT_SWIGLU;  // a gate of its columns' first half
+  product.tuning_config = a->tuning_config;
+  product.tuning_config_len = a->tuning_config_len;
+  const int st = product_plan(&product, pl);
+  if (st != GMMFR_OK) return st;
+  pl->p.act = a->activation;
+  pl->p.hidden = nullptr;
+  return kept_plan(a->kept, a->kept_scale, a->x.dtype, pl->p.m, pl->p.n / 2, &pl->p);
+}
+
+int backward_plan(const gmmgb_args* a, Plan* pl) {
+  if (!a) return GMMFR_ERR_NULLPTR;
+  if (!given(a->dy) || !given(a->w) || !given(a->group_list) || !given(a->kept) || !given(a->d)) return GMMFR_ERR_NULLPTR;
+  if (!in_16_bits(a->dy.dtype) || a->d.dtype != a->dy.dtype) return GMMFR_ERR_DTYPE;
+  if (given(a->h) && a->h.dtype != a->dy.dtype) return GMMFR_ERR_DTYPE;
+  if (a->activation != GMMGF_ACT_SWIGLU && a->activation != GMMGF_ACT_GEGLU) return GMMFR_ERR_ATTR;
+  if (a->d.ndim != 2 || a->d.dims[1] % 2 != 0) return GMMFR_ERR_SHAPE;
+  gmmgm_args product = {};
+  product.x = a->dy;
+  product.w = a->w;
+  product.group_list = a->group_list;
+  product.y = a->d;
+  product.y.dims[1] /= 2;  // the sums are dh
+  product.group_list_type = a->group_list_type;
+  product.transpose_w = a->transpose_w;
+  product.activation = GMMGM_ACT_NONE;
+  product.tuning_config = a->tuning_config;
+  product.tuning_config_len = a->tuning_config_len;
+  int st = product_plan(&product, pl);
+  if (st != GMMFR_OK) return st;
+  Params& p = pl->p;
+  if (given(a->h) && !shape_is(a->h, 2, p.m, p.n)) return GMMFR_ERR_SHAPE;
+  p.act = a->activation;
+  p.hidden = a->h.data;
+  st = aligned({&a->h});
+  return st != GMMFR_OK ? st : kept_plan(a->kept, a->kept_scale, a->dy.dtype, p.m, p.n, &p);
+}
+
+template <bool GLU, int FORM>
+int run(Plan& pl, void* stream) {
+  if (pl.p.m == 0) return GMMFR_OK;
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t done = pl.enc == kBf16 ? (pl.col ? launch<kBf16, false, true, false, GLU, FORM>(pl, s)
+                                                    : launch<kBf16, false, false, false, GLU, FORM>(pl, s))
+                                          : (pl.col ? launch<kF16, false, true, false, GLU, FORM>(pl, s)
+                                                    : launch<kF16, false, false, false, GLU, FORM>(pl, s));
+  return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+}
+
+int no_workspace(int status, size_t* workspace_bytes) {
+  if (status != GMMFR_OK) return status;
+  if (!workspace_bytes) return GMMFR_ERR_NULLPTR;
+  *workspace_bytes = 0;
+  return GMMFR_OK;
+}
+
+}  // namespace gmmgm
+
+extern "C" {
+
+using namespace gmmgm;
+
+int gmm_gated_matmul_workspace(const gmmgf_args* args, size_t* workspace_bytes) {
+  Plan pl;
+  return no_workspace(forward_plan(args, &pl), workspace_bytes);
+}
+
+int gmm_gated_matmul(const gmmgf_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  Plan pl;
+  const int st = forward_plan(args, &pl);
+  return st != GMMFR_OK ? st : run<true, kGated>(pl, stream);
+}
+
+int gmm_gated_matmul_backward_workspace(const gmmgb_args* args, size_t* workspace_bytes) {
+  Plan pl;
+  return no_workspace(backward_plan(args, &pl), workspace_bytes);
+}
+
+int gmm_gated_matmul_backward(const gmmgb_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  Plan pl;
+  const int st = backward_plan(args, &pl);
+  return st != GMMFR_OK ? st : run<false, kGatedBack>(pl, stream);
+}
+
+}  // extern "C"

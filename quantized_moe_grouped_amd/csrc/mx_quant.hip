@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "../../include/gmmfr.h"
+#include "mx_codes.h"
 
 namespace gmmmq {
 
@@ -53,18 +54,6 @@ template <int IN>
 __device__ __forceinline__ float value(uint32_t two, int i) {
   if constexpr (IN == kBf16) return __uint_as_float(i ? two & 0xFFFF0000u : two << 16);
   else return (float)__builtin_bit_cast(_Float16, (uint16_t)(i ? two >> 16 : two & 0xFFFFu));
-}
-
-// E8M0 code of a block whose largest magnitude has the fp32 bits `mag`: the
-// exponent field minus emax, at least 0; 255 when the block is not finite.
-template <bool FP8>
-__device__ __forceinline__ uint32_t scale_code(uint32_t mag) {
-  const uint32_t e = mag >> 23, emax = FP8 ? 8 : 2;
-  return e == 255 ? 255u : (e > emax ? e - emax : 0u);
-}
-// The power of two of an E8M0 code (0: 2^-127, a subnormal); NaN for 255.
-__device__ __forceinline__ float scale_value(uint32_t code) {
-  return __uint_as_float(code == 255 ? 0x7FC00000u : (code ? code << 23 : 0x00400000u));
 }
 
 // Codes of two values over the block's scale.  The FP4 conversion saturates by
