@@ -417,6 +417,32 @@ int gmm_grouped_matmul_wgrad_workspace(const gmmgw_args* args, size_t* workspace
 int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The same where one of the two was kept in FP8: the rows that the forward pass
+ * multiplied (gmm_mx_quantize), as x, or as dy for weights kept as (e,n,k).  A
+ * value is its code times its block's scale, brought to the other operand's
+ * type (exact in BFLOAT16, rounded to nearest in FLOAT16); the result is that
+ * of gmm_grouped_matmul_wgrad on such values, to the bit.
+ */
+typedef struct {
+  gmmfr_tensor x;           /* (m,k): BFLOAT16 or FLOAT16, or FLOAT8_E4M3FN          required */
+  gmmfr_tensor dy;          /* (m,n): the same; exactly one of the two is FLOAT8     required */
+  gmmfr_tensor x_scale;     /* FLOAT8_E8M0 (m,k/64,2)               given iff x is FLOAT8     */
+  gmmfr_tensor dy_scale;    /* FLOAT8_E8M0 (m,n/64,2)               given iff dy is FLOAT8    */
+  gmmfr_tensor group_list;  /* INT64 (e); type 0 cumulative ends, type 1 counts      required */
+  gmmfr_tensor dw;          /* out (e,k,n): the 16-bit operand's type or FLOAT32     required */
+  int64_t group_list_type;
+  int32_t accumulate;       /* 0 or 1 (FLOAT32 dw) */
+  int32_t reserved;
+  const int64_t* tuning_config; /* as gmm_grouped_matmul_wgrad's */
+  int64_t tuning_config_len;
+} gmmgx_args;
+
+/* Limits: those of gmm_grouped_matmul_wgrad, and 64 divides the columns of the
+ * FLOAT8 operand.  Two stages as there. */
+int gmm_grouped_matmul_wgrad_fp8_workspace(const gmmgx_args* args, size_t* workspace_bytes);
+int gmm_grouped_matmul_wgrad_fp8(const gmmgx_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The gated feed-forward block of the experts (e = 1: of a dense layer, or of a
  * shared expert), in training or in serving:
  *

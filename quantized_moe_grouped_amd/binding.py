@@ -30,7 +30,7 @@ EXPORTED = ("gmm_finalize_routing_workspace", "gmm_finalize_routing", "gmm_final
             "gmm_grouped_matmul_workspace", "gmm_grouped_matmul", "gmm_grouped_matmul_wgrad_workspace",
             "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize", "gmm_grouped_matmul_plan",
             "gmm_gated_matmul_workspace", "gmm_gated_matmul", "gmm_gated_matmul_backward_workspace",
-            "gmm_gated_matmul_backward")
+            "gmm_gated_matmul_backward", "gmm_grouped_matmul_wgrad_fp8_workspace", "gmm_grouped_matmul_wgrad_fp8")
 ACTIVATION = {None: 0, "none": 0, "swiglu": 1}
 GATE = {"swiglu": 1, "geglu": 2}  # of the gated block
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GMMFR_NOALLOC_SCRATCH_BYTES
@@ -84,6 +84,14 @@ class GmPlanInfo(ctypes.Structure):
 class GwArgs(ctypes.Structure):
     _fields_ = [
         ("x", Tensor), ("dy", Tensor), ("group_list", Tensor), ("dw", Tensor),
+        ("group_list_type", ctypes.c_int64), ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
+    ]
+
+
+class GxArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", Tensor), ("dy", Tensor), ("x_scale", Tensor), ("dy_scale", Tensor), ("group_list", Tensor), ("dw", Tensor),
         ("group_list_type", ctypes.c_int64), ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("tuning_config", ctypes.POINTER(ctypes.c_int64)), ("tuning_config_len", ctypes.c_int64),
     ]
@@ -147,7 +155,8 @@ def lib():
                                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
         L.gmm_quant_permute_profiled.restype = ctypes.c_int
         # arguments of these as void*: a struct by reference, or its bytes
-        for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad", "gmm_gated_matmul", "gmm_gated_matmul_backward"):
+        for name in ("gmm_grouped_matmul", "gmm_grouped_matmul_wgrad", "gmm_grouped_matmul_wgrad_fp8", "gmm_gated_matmul",
+                     "gmm_gated_matmul_backward"):
             getattr(L, name + "_workspace").argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]
             getattr(L, name + "_workspace").restype = ctypes.c_int
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
@@ -471,6 +480,11 @@ def _mq_bytes(x, codes, scales, transpose) -> bytes:
     return b"".join((_packed(x), _packed(codes), _packed(scales), _pack_ii(bool(transpose), 0)))
 
 
+def _gx_bytes(x, dy, x_scale, dy_scale, group_list, dw, group_list_type, accumulate, tail) -> bytes:
+    return b"".join((_packed(x), _packed(dy), _packed(x_scale), _packed(dy_scale), _packed(group_list), _packed(dw),
+                     _pack_qii(group_list_type, bool(accumulate), 0), tail))
+
+
 def _gf_bytes(x, w, group_list, h, kept, kept_scale, group_list_type, transpose_w, activation, tail) -> bytes:
     return b"".join((_packed(x), _packed(w), _packed(group_list), _packed(h), _packed(kept), _packed(kept_scale),
                      _pack_qii(group_list_type, bool(transpose_w), GATE[activation]), tail))
@@ -505,6 +519,14 @@ def make_gw_args(x, dy, group_list, dw, *, group_list_type: int = 0, accumulate:
     tuning, tail = _packed_tuning(tuning_config)
     raw = _gw_bytes(x, dy, group_list, dw, group_list_type, accumulate, tail)
     return GwArgs.from_buffer_copy(raw), (x, dy, group_list, dw, tuning)
+
+
+def make_gx_args(x, dy, group_list, dw, *, x_scale=None, dy_scale=None, group_list_type: int = 0,
+                 accumulate: bool = False, tuning_config: Optional[Sequence[int]] = None):
+    """C arguments of gmm_grouped_matmul_wgrad_fp8.  Returns (args, keepalive)."""
+    tuning, tail = _packed_tuning(tuning_config)
+    raw = _gx_bytes(x, dy, x_scale, dy_scale, group_list, dw, group_list_type, accumulate, tail)
+    return GxArgs.from_buffer_copy(raw), (x, dy, x_scale, dy_scale, group_list, dw, tuning)
 
 
 def make_gf_args(x, w, group_list, h, *, kept=None, kept_scale=None, group_list_type: int = 0,
@@ -613,30 +635,36 @@ def _grouped_matmul(handle, x, w, group_list, x_scale, w_scale, out, out_dtype, 
     return out
 
 
-def grouped_matmul_wgrad(x, dy, group_list, *, out=None, out_dtype=None, accumulate: bool = False,
-                         group_list_type: int = 0, tuning_config: Optional[Sequence[int]] = None, workspace=None,
-                         stream=None):
+def grouped_matmul_wgrad(x, dy, group_list, *, x_scale=None, dy_scale=None, out=None, out_dtype=None,
+                         accumulate: bool = False, group_list_type: int = 0,
+                         tuning_config: Optional[Sequence[int]] = None, workspace=None, stream=None):
     """Gradient of a grouped product's weights (e,k,n): x_g^T dy_g for every
     expert, in out_dtype (default fp32), zeros for one without rows.
     accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x).
-    With activation "swiglu" dy is the gradient of the product before it, which
-    no call here makes of the gradient behind it."""
-    dev = _check_tensors(x, dy, group_list, out, workspace)
+    One of the two may be in FP8 with its scales (x_scale or dy_scale, as
+    mx_quantize makes them): the result is that of the same values in the other
+    operand's type.  With a gate dy is the gradient of the product before it
+    (gated_matmul_backward)."""
+    dev = _check_tensors(x, dy, group_list, x_scale, dy_scale, out, workspace)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    return _on(dev, stream, _grouped_matmul_wgrad, x, dy, group_list, out, out_dtype, accumulate,
+    return _on(dev, stream, _grouped_matmul_wgrad, x, dy, group_list, x_scale, dy_scale, out, out_dtype, accumulate,
                group_list_type, tuning_config, workspace)
 
 
-def _grouped_matmul_wgrad(handle, x, dy, group_list, out, out_dtype, accumulate, group_list_type, tuning_config,
-                          workspace):
+def _grouped_matmul_wgrad(handle, x, dy, group_list, x_scale, dy_scale, out, out_dtype, accumulate, group_list_type,
+                          tuning_config, workspace):
     import torch
     if out is None:
         out = torch.empty((group_list.shape[0], x.shape[1], dy.shape[1]), dtype=out_dtype or torch.float32,
                           device=x.device)
     tuning, tail = _packed_tuning(tuning_config)
-    raw = _gw_bytes(x, dy, group_list, out, group_list_type, accumulate, tail)
-    _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
+    if x_scale is None and dy_scale is None:
+        raw = _gw_bytes(x, dy, group_list, out, group_list_type, accumulate, tail)
+        _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
+    else:
+        raw = _gx_bytes(x, dy, x_scale, dy_scale, group_list, out, group_list_type, accumulate, tail)
+        _enqueue("gmm_grouped_matmul_wgrad_fp8", raw, workspace, handle)
     del tuning
     return out
 

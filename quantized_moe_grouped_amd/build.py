@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libgmmfr.so")
 SOURCES = [os.path.join(CSRC, "gmmfr_kernels.hip"), os.path.join(CSRC, "gmmfr_api.cpp"),
            os.path.join(CSRC, "quant_permute.hip"), os.path.join(CSRC, "grouped_matmul.hip"),
            os.path.join(CSRC, "mx_quant.hip"),
-           os.path.join(CSRC, "gated_matmul.hip")]
+           os.path.join(CSRC, "gated_matmul.hip"), os.path.join(CSRC, "wgrad_fp8.hip")]
 ARCH = os.environ.get("GMMFR_ARCH", "gfx950")
 
 FLAGS = [

@@ -220,13 +220,14 @@ __device__ __forceinline__ void spread_fp8(v4u& d) {
   const auto b = __builtin_amdgcn_permlane32_swap(d.z, d.w, false, false);
   d = v4u{a[0], b[0], a[1], b[1]};
 }
-__device__ __forceinline__ void values_fp8(uint32_t d0, uint32_t d1, float scale, float (&v)[8]) {
+__device__ __forceinline__ void values_fp8(uint32_t d0, uint32_t d1, uint32_t scale, float (&v)[8]) {
   typedef float v2f __attribute__((ext_vector_type(2)));
+  const float s = __uint_as_float(scale << 23);  // the conversion takes the exponent, 0 as 2^-127 and 255 as NaN
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int four = (int)(q ? d1 : d0);
-    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(four, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(four, true);
-    v[4 * q] = lo.x * scale, v[4 * q + 1] = lo.y * scale, v[4 * q + 2] = hi.x * scale, v[4 * q + 3] = hi.y * scale;
+    const uint32_t four = q ? d1 : d0;
+    const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(four, s, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(four, s, true);
+    v[4 * q] = lo.x, v[4 * q + 1] = lo.y, v[4 * q + 2] = hi.x, v[4 * q + 3] = hi.y;
   }
 }
 

@@ -82,6 +82,8 @@ enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2 };
 // what becomes of a tile's sums: stored (with GLU through SwiGLU); the gated
 // block's forward pass (GLU) and its way back (the sums are dh)
 enum Form { kStore = 0, kGated = 1, kGatedBack = 2 };
+// weight gradient: the operand that is FP8 with a scale per 32 of its columns
+enum Eight { kNone8 = 0, kX8 = 1, kW8 = 2 };
 
 struct Params {
   const void* x;             // (m,k); 16-bit, FP8, or FP4 (m,k/2)
@@ -250,7 +252,7 @@ __device__ __forceinline__ void static_for(F&& f) {
 // own slice of every stage, and their sums meet in LDS (few rows: the weights
 // are streamed once and the tile is narrow).
 template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int BM, int BN, int BK, int WM, int WN, int STAGES,
-          bool KWAVES, int OCC, int FORM = kStore>
+          bool KWAVES, int OCC, int FORM = kStore, int EIGHT = kNone8>
 __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int NWAVES = WM * WN, NT = NWAVES * 64;
   constexpr bool MX = ENC == kFp4 || ENC == kFp8;
@@ -268,9 +270,19 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int XC = XCOL ? BM / 8 : BK * XBITS / 128, WC = WCOL ? BN / 8 : BK * WBITS / 128;
   constexpr int X_BYTES = BM * BK * XBITS / 8, W_BYTES = BN * BK * WBITS / 8;
   constexpr int XI = X_BYTES / 16 / NT, WI = W_BYTES / 16 / NT;  // copies of a thread for one stage
+  // An operand in FP8 (EIGHT): its codes are copied as they are, with their
+  // rows' scales, and each thread turns what it copied itself into 16-bit
+  // values for the stage that is multiplied next; two such stages are enough.
+  constexpr bool X8 = EIGHT == kX8, W8 = EIGHT == kW8;
+  static_assert(EIGHT == kNone8 || (WGRAD && STAGES % 2 == 0 && NS == 2), "FP8 rows are the weight gradient's");
+  constexpr int EB = X8 ? BM : BN, EC = EB / 16;               // its columns; 16-code chunks of a row
+  constexpr int E_BYTES = EB * BK, EI = E_BYTES / 16 / NT;      // codes of a stage, copies of a thread
+  constexpr int ER = 64 / EC, EROWS = EI * ER;                  // rows of a wave's copy, of all of them
+  constexpr int ED = EB / 128 + 1 <= 2 ? 2 : 4;                 // dwords that hold a row's scales, wherever they begin
+  static_assert(EIGHT == kNone8 || (EI >= 1 && EI * 16 * NT == E_BYTES && EROWS * ED <= 64), "whole copies");
   static_assert(XI >= 1 && WI >= 1 && XI * 16 * NT == X_BYTES && WI * 16 * NT == W_BYTES, "whole copies");
   static_assert((XCOL || NT / XC % 16 == 0) && (WCOL || NT / WC % 16 == 0), "one swizzle for all copies of a lane");
-  constexpr int STEP_COPIES = XI + WI;
+  constexpr int STEP_COPIES = (X8 ? EI + 1 : XI) + (W8 ? EI + 1 : WI);
   static_assert((STAGES - 2) * STEP_COPIES < 64, "vmcnt range");
   // E8M0 scales come a group at a time: with KWAVES 16 bytes a row (512
   // values), by copies; else 32 bytes (1024 values) into the registers of the
@@ -284,8 +296,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int SB = BK / 128;  // words of a row's scales in one step
   static_assert(!MX || KWAVES || SB == 1 || SB == 2, "words of a step");
 
-  __shared__ __attribute__((aligned(16))) uint8_t sX[STAGES * X_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t sW[STAGES * W_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sX[(X8 ? 2 : STAGES) * X_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sW[(W8 ? 2 : STAGES) * W_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t s_codes[EIGHT ? STAGES * E_BYTES : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t s_row_sc[EIGHT ? STAGES * NWAVES * 64 : 1];  // a wave's rows' scales
   // KWAVES: groups of scales as they lie in memory, from the dword that holds a
   // row's first one: up to STAGES - 1 in flight (a tile may end within a
   // group) and the one in use.  s_sc2: the dword after the 16 bytes, for rows
@@ -297,7 +311,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // KWAVES: the sums of one wave
   __shared__ __attribute__((aligned(16))) v4f s_sum[KWAVES ? FM * FN * 4 * 64 : 1];
   static_assert(NT > 256 || BM > 128 ||
-                    sizeof(sX) + sizeof(sW) + sizeof(s_sc) + sizeof(s_sc2) + sizeof(s_step) + sizeof(s_sum) +
+                    sizeof(sX) + sizeof(sW) + sizeof(s_codes) + sizeof(s_row_sc) + sizeof(s_sc) + sizeof(s_sc2) + sizeof(s_step) +
+                            sizeof(s_sum) +
                             (2 * kMaxExperts + 1) * 4 <= 80 * 1024,
                 "two workgroups a CU");
   extern __shared__ __attribute__((aligned(16))) int32_t s_dyn[];
@@ -310,9 +325,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   group_table(p, WGRAD ? 1 : BM, s_ends, s_pre);
   const int total = WGRAD ? p.e * p.tiles_m * p.tiles_n : s_pre[p.e];
   const int64_t F = GLU ? p.n / 2 : p.n;  // columns of y
-  const int64_t x_row = WGRAD ? p.k * 2 : p.k * XBITS / 8;  // bytes
-  const int64_t w_row = WCOL ? p.n * 2 : p.k * WBITS / 8;
-  const int64_t s_row = p.k / 32;
+  const int64_t x_row = WGRAD ? p.k * (X8 ? 1 : 2) : p.k * XBITS / 8;  // bytes
+  const int64_t w_row = WCOL ? p.n * (W8 ? 1 : 2) : p.k * WBITS / 8;
+  const int64_t s_row = (W8 ? p.n : p.k) / 32;
   const bool s_split = MX && (s_row & 3) != 0;  // k % 128 == 64: odd rows' scales begin mid-dword
 
   // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
@@ -393,9 +408,32 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   bool w_once = false;             // KWAVES: no other tile reads these weights
   uint32_t x_skip = 0, w_skip = 0; // rows across the reduction: bytes of a row before the tile
   uint32_t x_off[XI], w_off[WI], s_off[2] = {kOutside, kOutside}, s_odd[2] = {0, 0};
+  // EIGHT: offsets of the codes; the lane's row, dword of its scales and where
+  // they begin in the first of them, for the rows that the lane converts
+  const uint8_t* es_at = nullptr;
+  uint32_t es_skip = 0, e_off[EI > 0 ? EI : 1], es_off = kOutside, e_odd = 0, e_odd_next = 0;  // a bit per copy: 2 bytes in
+  const int es_row = EIGHT ? (lane / ED / ER) * (NT / EC) + wave * ER + lane / ED % ER : 0;
   const int x_ch = XCOL ? 0 : ((lane % XC) ^ swz_row<XC>(tid / XC)) * 16;
   const int w_ch = WCOL ? 0 : ((lane % WC) ^ swz_row<WC>(tid / WC)) * 16;
   auto cut = [](int64_t bytes) -> uint32_t { return (uint32_t)(bytes > (int64_t)kOutside ? (int64_t)kOutside : bytes); };
+  auto set_eight = [&](const Tile& c, int tid) {
+    if constexpr (EIGHT != kNone8) {
+      const int64_t row = X8 ? x_row : w_row;
+      const int first = X8 ? c.m0 : c.n0, left = X8 ? c.valid : (int)min((int64_t)BN, p.n - c.n0);
+      const uint8_t* at = (const uint8_t*)(X8 ? p.xs : p.ws) + (int64_t)c.r0 * s_row + first / 32;
+      const uint32_t in = (uintptr_t)at & 3;
+      es_at = at - in;
+      es_skip = first / 32 - in;  // (wraps: sizes below are taken modulo 2^32)
+      es_off = lane < EROWS * ED ? ((in + (uint32_t)es_row * (uint32_t)s_row) & ~3u) + lane % ED * 4 : kOutside;
+      e_odd_next = 0;
+#pragma unroll
+      for (int q = 0; q < EI; ++q) {
+        const int slot = q * NT + tid, r = slot / EC, col = slot % EC * 16;
+        e_off[q] = col < left ? (uint32_t)(r * (int)row + col) : kOutside;
+        e_odd_next |= ((in + (uint32_t)r * (uint32_t)s_row) & 2) << (2 * q);
+      }
+    }
+  };
   auto set_sources = [&](const Tile& c) {
     // indices pass through an opaque point: the offsets are computed here,
     // once a tile, and not kept in parts across the k-loop
@@ -403,11 +441,12 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     asm volatile("" : "+v"(lane), "+v"(tid));
     r_left = c.r1 - c.r0;
     w_once = c.alone;
+    set_eight(c, tid);
     if constexpr (XCOL) {  // wgrad: from (first row of the group, first column of the tile)
-      x_skip = c.m0 * 2;
+      x_skip = c.m0 * (X8 ? 1 : 2);
       x_at = (const uint8_t*)p.x + (int64_t)c.r0 * x_row + x_skip;
 #pragma unroll
-      for (int q = 0; q < XI; ++q) {
+      for (int q = 0; q < (X8 ? 0 : XI); ++q) {
         const int slot = q * NT + tid, r = slot / XC;
         const int col = ((slot % XC) ^ swz_col<XC>(r)) * 8;
         x_off[q] = col < c.valid ? (uint32_t)(r * (int)x_row + col * 2) : kOutside;
@@ -419,10 +458,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       for (int q = 0; q < XI; ++q) x_off[q] = (uint32_t)((q * (NT / XC) + tid / XC) * (int)x_row + x_ch);
     }
     if constexpr (WCOL) {  // from the tile's first column, of the expert's first row (or the group's)
-      w_skip = c.n0 * 2;
+      w_skip = c.n0 * (W8 ? 1 : 2);
       w_at = (const uint8_t*)p.w + (WGRAD ? (int64_t)c.r0 : c.g * p.k) * w_row + w_skip;
 #pragma unroll
-      for (int q = 0; q < WI; ++q) {
+      for (int q = 0; q < (W8 ? 0 : WI); ++q) {
         const int slot = q * NT + tid, r = slot / WC;
         const int col = column(c, ((slot % WC) ^ swz_col<WC>(r)) * 8);
         w_off[q] = col >= 0 ? (uint32_t)(r * (int)w_row + (col - c.n0) * 2) : kOutside;
@@ -537,7 +576,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   auto across = [&](uint32_t row, uint32_t skip) -> uint32_t {  // size of one stage's rows
     return r_left > 0 ? min(r_left, BK) * row - skip : 0u;
   };
-  auto issue_copy = [&](int st, auto q_) {
+  auto issue_whole = [&](int st, auto q_) {
     constexpr int Q = decltype(q_)::value;
     // in the last step of a reduction that is no multiple of BK, chunks past
     // the row's end would be the next row's
@@ -556,9 +595,26 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       else copy16(wr, off, to);
     }
   };
+  auto issue_copy = [&](int st, auto q_) {
+    constexpr int Q0 = decltype(q_)::value;
+    if constexpr (EIGHT && Q0 < EI) {
+      // an operand in FP8 goes first, as it is needed first, and its scales
+      const v4i r = buffer(X8 ? x_at : w_at, X8 ? across((uint32_t)x_row, x_skip) : across((uint32_t)w_row, w_skip));
+      copy16(r, e_off[Q0], __builtin_amdgcn_readfirstlane(lds_addr(s_codes)) + st * E_BYTES + (Q0 * NWAVES + wave) * 1024);
+    } else if constexpr (EIGHT && Q0 == EI) {
+      // up to the end of the dword that holds the last row's last; rows past it
+      // get zeros, whatever theirs would be: 2^-127 times codes of zero
+      const v4i r = buffer(es_at, r_left > 0 ? (min(r_left, BK) * (uint32_t)s_row - es_skip + 3) & ~3u : 0u);
+      copy4(r, es_row < r_left ? es_off : kOutside,
+            __builtin_amdgcn_readfirstlane(lds_addr(s_row_sc)) + (st * NWAVES + wave) * 256);
+    } else {
+      issue_whole(st, std::integral_constant<int, X8 ? Q0 - EI - 1 + XI : W8 ? Q0 - EI - 1 : Q0>{});
+    }
+  };
   auto advance = [&]() {
     x_at += XCOL ? BK * x_row : BK * XBITS / 8;
     w_at += WCOL ? BK * w_row : BK * WBITS / 8;
+    if constexpr (EIGHT) es_at += BK * s_row;
     // (never below nothing: past the last tile zeros are still copied)
     if constexpr (!XCOL) x_size = x_size > BK * XBITS / 8 ? x_size - BK * XBITS / 8 : 0;
     if constexpr (!WCOL) w_size = w_size > BK * WBITS / 8 ? w_size - BK * WBITS / 8 : 0;
@@ -621,7 +677,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // s: the slice (a constant once unrolled; the wave's own with KWAVES)
   auto read_frags = [&](int st, int s, XFrag (&xf)[FM], WFrag (&wf)[FN]) {
     constexpr int XP = XBITS == 8 ? 2 : 1;  // chunk pairs of a slice
-    const uint32_t xs = st * X_BYTES, ws = st * W_BYTES;
+    const uint32_t xs = (X8 ? st & 1 : st) * X_BYTES, ws = (W8 ? st & 1 : st) * W_BYTES;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if constexpr (XCOL) {
@@ -647,6 +703,44 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
     }
   };
+  // EIGHT: the codes of stage `st` that this thread copied, and their scales,
+  // once those copies have landed (the caller waits) ...
+  v4u e_raw[EI > 0 ? EI : 1];
+  uint32_t e_scale[EI > 0 ? EI : 1];
+  auto fetch_codes = [&](int st) {
+    if constexpr (EIGHT != kNone8) {
+      const int chunk = lane % EC;
+#pragma unroll
+      for (int q = 0; q < EI; ++q) {
+        e_raw[q] = *(const v4u*)(s_codes + st * E_BYTES + (q * NT + tid) * 16);
+        const uint8_t* sc = (const uint8_t*)(s_row_sc + (st * NWAVES + wave) * 64 + (q * ER + lane / EC) * ED);
+        e_scale[q] = sc[chunk / 2 + ((e_odd >> (2 * q)) & 2)];
+      }
+    }
+  };
+  // ... and half H of copy Q of them, eight values, into the stage's own place.
+  auto widen = [&](int st, auto part_) {
+    if constexpr (EIGHT != kNone8) {
+      constexpr int Q = decltype(part_)::value / 2, H = decltype(part_)::value % 2, C = X8 ? XC : WC;
+      const float scale = __uint_as_float(e_scale[Q] << 23);  // the conversions take the exponent, 0 as 2^-127 and 255 as NaN
+      v4u o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t four = e_raw[Q][2 * H + i / 2];
+        if constexpr (ENC == kBf16) {
+          o[i] = i % 2 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, scale, true))
+                       : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, scale, false));
+        } else {
+          o[i] = i % 2 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(four, scale, true))
+                       : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(four, scale, false));
+        }
+      }
+      const int slot = Q * NT + tid, r = slot / EC, chunk = 2 * (slot % EC) + H;
+      *(v4u*)((X8 ? sX + (st & 1) * X_BYTES : sW + (st & 1) * W_BYTES) + r * (C * 16) + ((chunk ^ swz_col<C>(r)) << 4)) = o;
+    }
+  };
+  constexpr int WIDEN = EIGHT ? 2 * EI : 0;  // pieces of a step
+
   // This step's scales, one register a fragment.  Slice q of a step takes its
   // blocks 2 q (lanes with h = 0) and 2 q + 1: of a step's bytes each lane
   // keeps every second one.  With four slices byte s is slice s's, with two it
@@ -826,7 +920,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     if (row >= c.valid || n >= F) return;
     const int64_t at = c.m0 + row;
     uint16_t* d = (uint16_t*)p.y + at * 2 * F;
-    const float gate_scale = gmmmq::scale_value(k.gate_scale), up_scale = gmmmq::scale_value(k.up_scale);
     if (p.keep == kKeepFp8) {
       spread_fp8(k.gate[0]);
       spread_fp8(k.up[0]);
@@ -837,8 +930,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
 #pragma unroll
       for (int r = 0; r < 8; ++r) dh[r] = sum_at(i, j, 8 * q + r);
       if (p.keep == kKeepFp8) {
-        values_fp8(k.gate[0][2 * q], k.gate[0][2 * q + 1], gate_scale, u);
-        values_fp8(k.up[0][2 * q], k.up[0][2 * q + 1], up_scale, v);
+        values_fp8(k.gate[0][2 * q], k.gate[0][2 * q + 1], k.gate_scale, u);
+        values_fp8(k.up[0][2 * q], k.up[0][2 * q + 1], k.up_scale, v);
       } else {
         values_16<ENC == kF16>(k.gate[q], u);
         values_16<ENC == kF16>(k.up[q], v);
@@ -1044,6 +1137,13 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     issue_scales(0, 0);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) all_copies(s);
+    if constexpr (EIGHT != kNone8) {
+      wait_vmcnt<YOUNGER>();
+      asm volatile("" ::: "memory");
+      e_odd = e_odd_next;
+      fetch_codes(0);
+      static_for<WIDEN>([&](auto w_) { widen(0, w_); });
+    }
     publish(0);
     issue_scales(1, 0);
     static_for<STEP_COPIES / PARTS>([&](auto q_) { issue_copy(STAGES - 1, q_); });
@@ -1056,8 +1156,23 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     // that share its SIMDs have them alone (2% at 1024 rows an expert).
     auto run = [&](auto alive_) {
       constexpr bool ALIVE = decltype(alive_)::value;
+      // the pieces of the coming step's FP8 operand that follow product m of the
+      // first slice, in its second half: their codes are on their way till then
+      auto widened = [&](auto part_, auto m_) {
+        if constexpr (EIGHT && decltype(part_)::value == 1) {
+          constexpr int M = decltype(m_)::value, H = PRODUCTS / 2;
+          if constexpr (M >= H) {
+            constexpr int A = WIDEN * (M - H) / H, B = WIDEN * (M - H + 1) / H;
+            static_for<B - A>([&](auto w_) { widen(st + 1, std::integral_constant<int, A + decltype(w_)::value>{}); });
+          }
+        }
+      };
       auto with_copies = [&](XFrag (&x)[FM], WFrag (&w)[FN], auto s_, auto part_) {
-        if constexpr (ALIVE) multiply(x, w, s_, [&](auto m_) { copies(refill, part_, m_); });
+        if constexpr (ALIVE)
+          multiply(x, w, s_, [&](auto m_) {
+            copies(refill, part_, m_);
+            widened(part_, m_);
+          });
         else static_for<PRODUCTS>([&](auto m_) { copies(refill, part_, m_); });
       };
 #pragma unroll 1
@@ -1065,6 +1180,14 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
         static_for<NS - 1>([&](auto s_) {
           constexpr int S = decltype(s_)::value;
           if constexpr (ALIVE) read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+          if constexpr (EIGHT != kNone8) {
+            // issued by now: this step's copies and the next two's, and half of
+            // those of the one after; wanted: the next one's first EI + 1
+            wait_vmcnt<STEP_COPIES * 2 + STEP_COPIES / 2 - EI - 1>();
+            asm volatile("" ::: "memory");
+            if (kt + 1 == steps) e_odd = e_odd_next;
+            fetch_codes(st + 1 == STAGES ? 0 : st + 1);
+          }
           if constexpr (S == 0 && PARTS == 2) {
             with_copies(xf[0], wf[0], s_, Second{});
             advance();

@@ -139,3 +139,45 @@ def test_a_lost_gradient_is_refused(which):
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def gx(m=300, k=512, n=384, e=4, dt=BF, side="x", **over):
+    a = B.GxArgs()
+    a.x, a.dy, a.group_list, a.dw = fake(dt, m, k), fake(dt, m, n), fake(I64, e), fake(F32, e, k, n)
+    if side == "x":
+        a.x, a.x_scale = fake(FP8, m, k), fake(E8, m, k // 64, 2)
+    else:
+        a.dy, a.dy_scale = fake(FP8, m, n), fake(E8, m, n // 64, 2)
+    return put(a, over)
+
+
+GX_CASES = [
+    ({}, B.OK), (dict(side="dy"), B.OK), (dict(dt=F16), B.OK), (dict(m=0), B.OK), (dict(accumulate=1), B.OK), (dict(n=8), B.OK),
+    (dict(side="dy", k=8), B.OK), (dict(dw=fake(BF, 4, 512, 384)), B.OK), (dict(tuning=[0, 128, 4]), B.OK),
+    (dict(x=NONE), B.ERR_NULLPTR), (dict(dy=NONE), B.ERR_NULLPTR), (dict(dw=NONE), B.ERR_NULLPTR), (dict(group_list=NONE), B.ERR_NULLPTR),
+    (dict(x_scale=NONE), B.ERR_NULLPTR), (dict(side="dy", dy_scale=NONE), B.ERR_NULLPTR),
+    (dict(x=fake(BF, 300, 512)), B.ERR_DTYPE), (dict(dy=fake(FP8, 300, 384)), B.ERR_DTYPE), (dict(dt=F32), B.ERR_DTYPE),
+    (dict(x=fake(FP4, 300, 256)), B.ERR_DTYPE), (dict(x_scale=fake(F32, 300, 8, 2)), B.ERR_DTYPE), (dict(dw=fake(F16, 4, 512, 384)), B.ERR_DTYPE),
+    (dict(dy_scale=fake(E8, 300, 6, 2)), B.ERR_UNSUPPORTED), (dict(side="dy", x_scale=fake(E8, 300, 8, 2)), B.ERR_UNSUPPORTED),
+    (dict(accumulate=2), B.ERR_ATTR), (dict(accumulate=1, dw=fake(BF, 4, 512, 384)), B.ERR_ATTR), (dict(group_list_type=3), B.ERR_ATTR),
+    (dict(tuning=[0, 32]), B.ERR_ATTR),
+    (dict(k=520), B.ERR_SHAPE), (dict(side="dy", n=392), B.ERR_SHAPE), (dict(n=12), B.ERR_SHAPE), (dict(x_scale=fake(E8, 300, 16)), B.ERR_SHAPE),
+    (dict(x_scale=fake(E8, 299, 8, 2)), B.ERR_SHAPE), (dict(e=1025), B.ERR_SHAPE), (dict(dw=fake(F32, 4, 384, 512)), B.ERR_SHAPE),
+    (dict(x=fake(FP8, 300, 512, ptr=0x7000008)), B.ERR_ALIGN), (dict(x_scale=fake(E8, 300, 8, 2, ptr=0x7000002)), B.ERR_ALIGN),
+]
+
+
+@pytest.mark.parametrize("over,code", GX_CASES, ids=[str(i) for i in range(len(GX_CASES))])
+def test_wgrad_fp8_stage_one(over, code):
+    sizes = {k: v for k, v in over.items() if k in ("m", "k", "n", "e", "dt", "side")}
+    a = gx(**sizes, **{k: v for k, v in over.items() if k not in sizes})
+    assert stage_one("gmm_grouped_matmul_wgrad_fp8", a) == (code, 0 if code == B.OK else 12345)
+    if code != B.OK:
+        assert B.lib().gmm_grouped_matmul_wgrad_fp8(ctypes.byref(a), None, 0, None) == code
+
+
+def test_wgrad_fp8_null_pointers():
+    L, a = B.lib(), gx()
+    assert L.gmm_grouped_matmul_wgrad_fp8_workspace(None, ctypes.byref(ctypes.c_size_t())) == B.ERR_NULLPTR
+    assert L.gmm_grouped_matmul_wgrad_fp8_workspace(ctypes.byref(a), None) == B.ERR_NULLPTR
+    assert L.gmm_grouped_matmul_wgrad_fp8(None, None, 0, None) == B.ERR_NULLPTR
