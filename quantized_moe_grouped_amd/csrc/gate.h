@@ -209,10 +209,7 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, uint8_t* scales, int n, 
   *(v4u*)(row + n + 16 * (lane >> 5)) = v4u{a[0], a[1], b[0], b[1]};
   if (lane < 32) scales[n / 32] = (uint8_t)code;
 }
-__device__ __forceinline__ void load_fp8(const uint8_t* row, const uint8_t* scales, int n, int lane, v4u (&d)[2], uint32_t& scale) {
-  d[0] = *(const v4u*)(row + n + 16 * (lane >> 5));
-  scale = scales[n / 32];
-}
+__device__ __forceinline__ v4u load_fp8(const uint8_t* row, int n, int lane) { return *(const v4u*)(row + n + 16 * (lane >> 5)); }
 // Brings the codes back to the lanes that compute: dwords 2 q and 2 q + 1 hold
 // piece q's eight.
 __device__ __forceinline__ void spread_fp8(v4u& d) {
@@ -231,10 +228,10 @@ __device__ __forceinline__ void values_fp8(uint32_t d0, uint32_t d1, uint32_t sc
   }
 }
 
-// What was kept of a block, as it lies in memory: two pieces of each half in 16
-// bits, or one and the scale in FP8.
+// What was kept of a block's two halves, as it lies in memory.
+template <bool FP8>
 struct Kept {
-  v4u gate[2], up[2];
+  v4u gate[FP8 ? 1 : 2], up[FP8 ? 1 : 2];
   uint32_t gate_scale, up_scale;
 };
 

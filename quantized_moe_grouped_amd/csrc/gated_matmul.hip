@@ -133,7 +133,8 @@ int gmm_gated_matmul_backward(const gmmgb_args* args, void* workspace, size_t wo
   (void)workspace_bytes;
   Plan pl;
   const int st = backward_plan(args, &pl);
-  return st != GMMFR_OK ? st : run<false, kGatedBack>(pl, stream);
+  if (st != GMMFR_OK) return st;
+  return pl.p.keep == kKeepFp8 ? run<false, kBackFp8>(pl, stream) : run<false, kBackFull>(pl, stream);
 }
 
 }  // extern "C"

@@ -80,8 +80,9 @@ constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every descri
 enum Enc { kBf16 = 0, kF16 = 1, kFp4 = 2, kFp8 = 3 };  // of the rows; weights: the same, or FP4 with kFp4 and kFp8
 enum Out { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2 };
 // what becomes of a tile's sums: stored (with GLU through SwiGLU); the gated
-// block's forward pass (GLU) and its way back (the sums are dh)
-enum Form { kStore = 0, kGated = 1, kGatedBack = 2 };
+// block's forward pass (GLU) and its way back (the sums are dh) from what was
+// kept in 16 bits or in FP8
+enum Form { kStore = 0, kGated = 1, kBackFull = 2, kBackFp8 = 3 };
 // weight gradient: the operand that is FP8 with a scale per 32 of its columns
 enum Eight { kNone8 = 0, kX8 = 1, kW8 = 2 };
 
@@ -675,32 +676,54 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     return v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   };
   // s: the slice (a constant once unrolled; the wave's own with KWAVES)
-  auto read_frags = [&](int st, int s, XFrag (&xf)[FM], WFrag (&wf)[FN]) {
+  auto read_x = [&](int st, int s, int i, XFrag& f) {
     constexpr int XP = XBITS == 8 ? 2 : 1;  // chunk pairs of a slice
-    const uint32_t xs = (X8 ? st & 1 : st) * X_BYTES, ws = (W8 ? st & 1 : st) * W_BYTES;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if constexpr (XCOL) {
-        xf[i] = frag_col(x_adr[i] + xs + s * (16 * XC * 16), XC * 16);
-      } else if constexpr (KWAVES) {
-        const int row = i * 32 + (lane & 31);
-        constexpr auto c = std::integral_constant<int, XCOL ? 8 : XC>{};
-        const uint32_t at = lds_addr(sX) + xs;
-        frag_row(at + row_adr(row, s * XP, c), at + row_adr(row, s * XP + XP - 1, c), &xf[i]);
-      } else {
-        const uint32_t at = xs + i * (32 * XC * 16);
-        frag_row(x_adr[s * XP] + at, x_adr[s * XP + XP - 1] + at, &xf[i]);
-      }
+    const uint32_t xs = (X8 ? st & 1 : st) * X_BYTES;
+    if constexpr (XCOL) {
+      f = frag_col(x_adr[i] + xs + s * (16 * XC * 16), XC * 16);
+    } else if constexpr (KWAVES) {
+      const int row = i * 32 + (lane & 31);
+      constexpr auto c = std::integral_constant<int, XCOL ? 8 : XC>{};
+      const uint32_t at = lds_addr(sX) + xs;
+      frag_row(at + row_adr(row, s * XP, c), at + row_adr(row, s * XP + XP - 1, c), &f);
+    } else {
+      const uint32_t at = xs + i * (32 * XC * 16);
+      frag_row(x_adr[s * XP] + at, x_adr[s * XP + XP - 1] + at, &f);
     }
+  };
+  auto read_w = [&](int st, int s, int j, WFrag& f) {
+    const uint32_t ws = (W8 ? st & 1 : st) * W_BYTES;
+    if constexpr (WCOL) {
+      f = frag_col(w_adr[j] + ws + s * (16 * WC * 16), WC * 16);
+    } else if constexpr (KWAVES) {
+      frag_row(lds_addr(sW) + ws + row_adr(j * 32 + (lane & 31), s, std::integral_constant<int, WCOL ? 8 : WC>{}), 0, &f);
+    } else {
+      frag_row(w_adr[s] + ws + j * (32 * WC * 16), 0, &f);
+    }
+  };
+  auto read_frags = [&](int st, int s, XFrag (&xf)[FM], WFrag (&wf)[FN]) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      if constexpr (WCOL) {
-        wf[j] = frag_col(w_adr[j] + ws + s * (16 * WC * 16), WC * 16);
-      } else if constexpr (KWAVES) {
-        frag_row(lds_addr(sW) + ws + row_adr(j * 32 + (lane & 31), s, std::integral_constant<int, WCOL ? 8 : WC>{}), 0, &wf[j]);
-      } else {
-        frag_row(w_adr[s] + ws + j * (32 * WC * 16), 0, &wf[j]);
-      }
+    for (int i = 0; i < FM; ++i) read_x(st, s, i, xf[i]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_w(st, s, j, wf[j]);
+  };
+  // Those of them that are read after product m of the slice before, in the
+  // order in which the products want them: in the first half of the slice, one
+  // or two after a product.  All at once they hold the LDS, and with it every
+  // wave's issue, before the first product.
+  auto read_after = [&](int st, int s, XFrag (&xf)[FM], WFrag (&wf)[FN], auto m_) {
+    constexpr int M = decltype(m_)::value, ALL = FM + FN, HALF = FM * FN / 2;
+    constexpr int A = ALL * M / HALF < ALL ? ALL * M / HALF : ALL, B = ALL * (M + 1) / HALF < ALL ? ALL * (M + 1) / HALF : ALL;
+    if constexpr (B > A) {
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<B - A>([&](auto q_) {
+        constexpr int Q = A + decltype(q_)::value;  // w0 x0 w1 .. x1 ..
+        if constexpr (Q == 0) read_w(st, s, 0, wf[0]);
+        else if constexpr (Q == 1) read_x(st, s, 0, xf[0]);
+        else if constexpr (Q <= FN) read_w(st, s, Q - 1, wf[Q - 1]);
+        else read_x(st, s, Q - FN, xf[Q - FN]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   // EIGHT: the codes of stage `st` that this thread copied, and their scales,
@@ -896,31 +919,31 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     else swiglu16(u, v, o);
     store_16<ENC == kF16>((uint16_t*)p.y + at * F, n, width, lane, o);
   };
-  // One block of the way back; `k`: what was kept for it (load_kept).
-  auto load_kept = [&](const Tile& c, int lane, int i, int col) -> Kept {
-    Kept k{};
-    const int row = wm * WTM + i * 32 + (lane & 31);
-    if (row >= c.valid || c.n0 + col >= F) return k;
+  // One block of the way back; `k`: what was kept for it.
+  constexpr bool BACK = FORM == kBackFull || FORM == kBackFp8, BACK8 = FORM == kBackFp8;
+  auto load_kept = [&](const Tile& c, int lane, int i, int j, Kept<BACK8>& k) {
+    const int row = wm * WTM + i * 32 + (lane & 31), n = c.n0 + wn * WTN + j * 32, width = (int)F;
+    if (row >= c.valid || n >= F) return;
     const int64_t at = c.m0 + row;
-    const int n = c.n0 + col, width = (int)F;
-    if (p.keep == kKeepFp8) {
+    if constexpr (BACK8) {
       const uint8_t* codes = (const uint8_t*)p.kept + at * 2 * F;
-      const uint8_t* scales = p.kept_scale + at * (F / 16);
-      load_fp8(codes, scales, n, lane, k.gate, k.gate_scale);
-      load_fp8(codes + F, scales + F / 32, n, lane, k.up, k.up_scale);
+      const uint8_t* scales = p.kept_scale + at * (F / 16) + n / 32;
+      k.gate[0] = load_fp8(codes, n, lane);
+      k.up[0] = load_fp8(codes + F, n, lane);
+      k.gate_scale = scales[0];
+      k.up_scale = scales[F / 32];
     } else {
       const uint16_t* kept = (const uint16_t*)p.kept + at * 2 * F;
       load_16(kept, n, width, lane, k.gate);
       load_16(kept + F, n, width, lane, k.up);
     }
-    return k;
   };
-  auto back_block = [&](const Tile& c, int lane, int i, int j, Kept& k) {
+  auto back_block = [&](const Tile& c, int lane, int i, int j, Kept<BACK8> k, const float (&sums)[16]) {
     const int row = wm * WTM + i * 32 + (lane & 31), n = c.n0 + wn * WTN + j * 32, width = (int)F;
     if (row >= c.valid || n >= F) return;
     const int64_t at = c.m0 + row;
     uint16_t* d = (uint16_t*)p.y + at * 2 * F;
-    if (p.keep == kKeepFp8) {
+    if constexpr (BACK8) {
       spread_fp8(k.gate[0]);
       spread_fp8(k.up[0]);
     }
@@ -928,8 +951,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     for (int q = 0; q < 2; ++q) {
       float dh[8], u[8], v[8], h[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) dh[r] = sum_at(i, j, 8 * q + r);
-      if (p.keep == kKeepFp8) {
+      for (int r = 0; r < 8; ++r) dh[r] = sums[8 * q + r];
+      if constexpr (BACK8) {
         values_fp8(k.gate[0][2 * q], k.gate[0][2 * q + 1], k.gate_scale, u);
         values_fp8(k.up[0][2 * q], k.up[0][2 * q + 1], k.up_scale, v);
       } else {
@@ -950,15 +973,35 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     // sum_at's asm reads products' results: past the 18 wait states that the
     // last of them may need
     if constexpr (IN_AGPRS) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-    if constexpr (FORM == kGatedBack) {
-      // what was kept for the next block is on its way while one is computed
-      Kept next = load_kept(c, lane, 0, wn * WTN);
+    if constexpr (BACK) {
+      // What was kept is asked for AHEAD blocks before it is used: loads and
+      // stores are counted together and in order, so that a load behind stores
+      // is waited for with them.
+      // One loop over the blocks, whose sums are brought to the same registers:
+      // unrolled it would be 30 KB of instructions that every wave fetches once
+      // a tile.  What was kept is asked for three blocks ahead: loads and stores
+      // are counted together and in order, so that a load is waited for with the
+      // stores before it.
+      constexpr int BLOCKS = FM * FN;
+      auto ask = [&](int b) -> Kept<BACK8> {
+        Kept<BACK8> k;
+        if (b < BLOCKS) load_kept(c, lane, b / FN, b % FN, k);
+        return k;
+      };
+      Kept<BACK8> k0 = ask(0), k1 = ask(1), k2 = ask(2);
+#pragma unroll 1
+      for (int b = 0; b < BLOCKS; ++b) {
+        const Kept<BACK8> k3 = ask(b + 3);
+        float sums[16];
+        static_for<BLOCKS>([&](auto b_) {
+          constexpr int B = decltype(b_)::value;
+          if (b == B) {
 #pragma unroll
-      for (int b = 0; b < FM * FN; ++b) {
-        Kept now = next;
-        if (b + 1 < FM * FN) next = load_kept(c, lane, (b + 1) / FN, wn * WTN + (b + 1) % FN * 32);
-        __builtin_amdgcn_sched_barrier(0);
-        back_block(c, lane, b / FN, b % FN, now);
+            for (int r = 0; r < 16; ++r) sums[r] = sum_at(B / FN, B % FN, r);
+          }
+        });
+        back_block(c, lane, b / FN, b % FN, k0, sums);
+        k0 = k1, k1 = k2, k2 = k3;
       }
       return;
     }
@@ -1167,9 +1210,11 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           }
         }
       };
-      auto with_copies = [&](XFrag (&x)[FM], WFrag (&w)[FN], auto s_, auto part_) {
+      auto with_copies = [&](XFrag (&x)[FM], WFrag (&w)[FN], auto s_, auto part_, int to, auto t_) {
+        constexpr int T = decltype(t_)::value;  // the slice whose fragments are read meanwhile, of stage `to`
         if constexpr (ALIVE)
           multiply(x, w, s_, [&](auto m_) {
+            read_after(to, T, xf[T & 1], wf[T & 1], m_);
             copies(refill, part_, m_);
             widened(part_, m_);
           });
@@ -1179,7 +1224,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       for (int kt = 0; kt < steps; ++kt) {
         static_for<NS - 1>([&](auto s_) {
           constexpr int S = decltype(s_)::value;
-          if constexpr (ALIVE) read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
           if constexpr (EIGHT != kNone8) {
             // issued by now: this step's copies and the next two's, and half of
             // those of the one after; wanted: the next one's first EI + 1
@@ -1189,10 +1233,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
             fetch_codes(st + 1 == STAGES ? 0 : st + 1);
           }
           if constexpr (S == 0 && PARTS == 2) {
-            with_copies(xf[0], wf[0], s_, Second{});
+            with_copies(xf[0], wf[0], s_, Second{}, st, std::integral_constant<int, S + 1>{});
             advance();
           } else if constexpr (ALIVE) {
-            multiply(xf[S & 1], wf[S & 1], s_, nothing);
+            multiply(xf[S & 1], wf[S & 1], s_, [&](auto m_) { read_after(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1], m_); });
           }
         });
         publish(kt + 1 < steps ? kt + 1 : 0);
@@ -1214,11 +1258,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           }
           issue_scales(kt + 2 < steps ? kt + 2 : kt + 2 - steps, 0);
         }
-        if constexpr (ALIVE) {
-          fetch_scales(slot);
-          read_frags(st, 0, xf[0], wf[0]);
-        }
-        with_copies(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{}, First{});
+        if constexpr (ALIVE) fetch_scales(slot);
+        with_copies(xf[(NS - 1) & 1], wf[(NS - 1) & 1], std::integral_constant<int, NS - 1>{}, First{}, st, First{});
         if constexpr (PARTS == 1) advance();
         if constexpr (ALIVE) keep_scales();
       }
@@ -1241,6 +1282,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       if (t_next < 0) break;
       c = next;
       steps = steps_of(c);
+      // the way back wants its registers for itself: the next tile's first
+      // fragments are read again
+      if constexpr (BACK) read_frags(st, 0, xf[0], wf[0]);
     }
   }
   wait_vmcnt<0>();  // no copy in flight when the workgroup ends
@@ -1469,6 +1513,7 @@ hipError_t launch(Plan& pl, hipStream_t s) {
   const size_t dyn = (size_t)(2 * pl.p.e + 1) * 4;
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
   constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
+  constexpr bool FOUR = WGRAD || FORM == kBackFull || FORM == kBackFp8;  // waves of 128 x 128
   void* args[] = {&pl.p};
   if (pl.kind == kLarge)
     // The weight gradient's stages are whole rows of a tile whatever their
@@ -1478,8 +1523,8 @@ hipError_t launch(Plan& pl, hipStream_t s) {
     // of 128 x 128 read a third less from LDS than eight of 64 x 128, which
     // transposing reads make up for (1.20 -> 1.12 ms; without them -1 .. +2%).
     return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK,
-                                                       WGRAD ? 2 : 4, 2, WGRAD ? 4 : 2, false, WGRAD ? 1 : 2, FORM>,
-                           dim3(pl.grid), dim3(WGRAD ? 256 : 512), args, dyn, s);
+                                                       FOUR ? 2 : 4, 2, WGRAD ? 4 : 2, false, FOUR ? 1 : 2, FORM>,
+                           dim3(pl.grid), dim3(FOUR ? 256 : 512), args, dyn, s);
   if constexpr (!WGRAD) {
     if (pl.kind == kSmall)
       return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, STS, true, 2, FORM>,
