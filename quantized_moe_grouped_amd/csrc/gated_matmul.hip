@@ -79,6 +79,7 @@ int backward_plan(const gmmgb_args* a, Plan* pl) {
   int st = product_plan(&product, pl);
   if (st != GMMFR_OK) return st;
   Params& p = pl->p;
+  if (p.n > 32768) return GMMFR_ERR_SHAPE;  // 2 f, as in the forward pass
   if (given(a->h) && !shape_is(a->h, 2, p.m, p.n)) return GMMFR_ERR_SHAPE;
   p.act = a->activation;
   p.hidden = a->h.data;

@@ -246,6 +246,17 @@ __device__ __forceinline__ void static_for(F&& f) {
   }
 }
 
+// f(i) of the i in [LO, HI) that is known only when it runs, by halving.
+template <int LO, int HI, typename F>
+__device__ __forceinline__ void one_of(int i, F&& f) {
+  if constexpr (HI - LO == 1) {
+    f(std::integral_constant<int, LO>{});
+  } else {
+    if (i < (LO + HI) / 2) one_of<LO, (LO + HI) / 2>(i, f);
+    else one_of<(LO + HI) / 2, HI>(i, f);
+  }
+}
+
 // ENC: operand encoding.  XCOL / WCOL: the operand's fast axis is M / N (16
 // bit only) instead of the reduction.  WGRAD: see above.  GLU: SwiGLU
 // epilogue; the tile's columns alternate 32 gate columns and the 32 up columns
@@ -993,12 +1004,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       for (int b = 0; b < BLOCKS; ++b) {
         const Kept<BACK8> k3 = ask(b + 3);
         float sums[16];
-        static_for<BLOCKS>([&](auto b_) {
+        one_of<0, BLOCKS>(b, [&](auto b_) {
           constexpr int B = decltype(b_)::value;
-          if (b == B) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sums[r] = sum_at(B / FN, B % FN, r);
-          }
+          for (int r = 0; r < 16; ++r) sums[r] = sum_at(B / FN, B % FN, r);
         });
         back_block(c, lane, b / FN, b % FN, k0, sums);
         k0 = k1, k1 = k2, k2 = k3;
@@ -1448,7 +1457,11 @@ inline int product_plan(const gmmgm_args* a, Plan* pl) {
   const int64_t middle = busy * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
   const bool narrow = avg <= 16 ? !pl->col || middle <= 256
                                 : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256));
+  // One expert's rows are known but for those behind it: whole tiles of them
+  // (4096 rows of 7168 bf16 (e,n,k), us under 128-row and 256-row tiles: n =
+  // 4096 with a gate 218, 183, n = 2048 112, 135).
   auto along = [&](int64_t t) {
+    if (parts == 1) return 2 * ceil_div(rows > 0 ? rows : m, t);
     if (rows > 0) return 2 * busy * ceil_div(rows, t);
     return 4 * m <= 3 * t * busy ? 2 * busy : 2 * m / t + busy;
   };
@@ -1498,7 +1511,13 @@ inline int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   pl->enc = xt == GMMFR_DT_BFLOAT16 ? kBf16 : kF16;
   pl->glu = false;
   pl->col = true;
+  // Few rows an expert are a few steps: with results of 16 bits, which do not
+  // fill the memory's time, two workgroups a CU hide the tiles' ends (us under
+  // 128-row and 256-row tiles, 32 experts of 2048 x 2048, bf16 results: 8 rows
+  // 71, 85, 64 rows 94, 94, 128 rows 115, 111; fp32: 8 rows 148, 110).
+  const bool few = ot != GMMFR_DT_FLOAT32 && m <= 64 * e;
   pl->kind = height ? (height == 256 ? kLarge : kMiddle)
+             : few  ? kMiddle
                     : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n, false);
   p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);
   p.tiles_n = (int32_t)ceil_div(n, kTileN[pl->kind]);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from quantized_moe_grouped_amd import binding as B
-from tests.test_boundary_grouped import BF, E8, F16, F32, FP4, FP8, I64, fake, put, stage_one
+from tests.test_boundary_grouped import BF, E8, F16, F32, FP4, FP8, I64, fake, gm, put, stage_one
 
 NONE = B.Tensor()
 
@@ -61,6 +61,7 @@ CASES = [
     (gf, dict(k=65536, f=32768, transpose_w=1, w=fake(BF, 4, 65536, 65536)), B.ERR_SHAPE),
     (gb, dict(d=fake(BF, 300, 192)), B.ERR_SHAPE), (gb, dict(d=fake(BF, 300, 383)), B.ERR_SHAPE), (gb, dict(h=fake(BF, 300, 384)), B.ERR_SHAPE),
     (gb, dict(kept=fake(BF, 301, 384)), B.ERR_SHAPE), (gb, dict(f=36), B.ERR_SHAPE), (gb, dict(d=fake(BF, 300, 384, 1)), B.ERR_SHAPE),
+    (gf, dict(f=32768, k=8), B.OK), (gb, dict(f=32768, k=8), B.OK), (gf, dict(f=32776, k=8), B.ERR_SHAPE), (gb, dict(f=32776, k=8), B.ERR_SHAPE),
     (gb, dict(transpose_w=0), B.ERR_SHAPE), (gb, dict(f=40, **in_fp8(300, 40)), B.ERR_SHAPE),
     (gf, dict(h=fake(BF, 300, 192, ptr=0x7000008)), B.ERR_ALIGN), (gf, dict(kept=fake(BF, 300, 384, ptr=0x7000002)), B.ERR_ALIGN),
     (gb, dict(h=fake(BF, 300, 192, ptr=0x7000008)), B.ERR_ALIGN), (gb, dict(kept=fake(BF, 300, 384, ptr=0x7000002)), B.ERR_ALIGN),
@@ -181,3 +182,11 @@ def test_wgrad_fp8_null_pointers():
     assert L.gmm_grouped_matmul_wgrad_fp8_workspace(None, ctypes.byref(ctypes.c_size_t())) == B.ERR_NULLPTR
     assert L.gmm_grouped_matmul_wgrad_fp8_workspace(ctypes.byref(a), None) == B.ERR_NULLPTR
     assert L.gmm_grouped_matmul_wgrad_fp8(None, None, 0, None) == B.ERR_NULLPTR
+
+
+@pytest.mark.parametrize("n,tile", [(4096, 256), (2048, 128)])
+def test_one_experts_rows_are_whole_tiles(n, tile):
+    """4096 rows are 16 tiles of 256: with 4096 columns one round of the chip,
+    with 2048 half a round, where 128-row tiles make a whole one."""
+    for rows in ([], [4096], [0]):
+        assert B.gm_plan(gm(m=4096, k=7168, n=n, e=1, **(dict(tuning=rows) if rows else {})))["tile_m"] == tile
