@@ -32,20 +32,21 @@ __device__ __forceinline__ float swiglu_far(float u, float v) {
   const float h = __builtin_amdgcn_exp2f(u * 0.72134752f);
   return u * h * v * h;
 }
-// For a lane's 16 values.  Gates below -87 are rare: both forms, and a choice for
+// For a lane's values.  Gates below -87 are rare: both forms, and a choice for
 // each value by its own gate alone, only where a lane of the wave has one (a form
 // right for all gates, taken for all: 1.3%, FP4, 131072 x 7168 x 4096 over 32
 // experts, 2034 -> 2060 us; the test of the gates 0.5%).
-__device__ __forceinline__ void swiglu16(const float (&u)[16], const float (&v)[16], float (&o)[16]) {
+template <int N>
+__device__ __forceinline__ void swiglus(const float (&u)[N], const float (&v)[N], float (&o)[N]) {
   uint32_t least = 0;  // the most negative gate has the largest bits
 #pragma unroll
-  for (int r = 0; r < 16; ++r) least = max(least, __float_as_uint(u[r]));
+  for (int r = 0; r < N; ++r) least = max(least, __float_as_uint(u[r]));
   if (__any(least > __float_as_uint(-87.0f))) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[r] = u[r] < -87.0f ? swiglu_far(u[r], v[r]) : swiglu(u[r], v[r]);
+    for (int r = 0; r < N; ++r) o[r] = u[r] < -87.0f ? swiglu_far(u[r], v[r]) : swiglu(u[r], v[r]);
   } else {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[r] = swiglu(u[r], v[r]);
+    for (int r = 0; r < N; ++r) o[r] = swiglu(u[r], v[r]);
   }
 }
 
@@ -61,23 +62,24 @@ __device__ __forceinline__ float gelu_square(float u) { return fminf(u * u, 256.
 __device__ __forceinline__ float gelu_exponent(float u, float square) {  // -z log2(e)
   return u * __builtin_fmaf(square, -kGeluLog2 * kGeluCube, -kGeluLog2);
 }
-// As swiglu16, with gelu: past z = -87 with exp(z / 2) twice.
-__device__ __forceinline__ void geglu16(const float (&u)[16], const float (&v)[16], float (&o)[16]) {
-  float t[16], most = 0.0f;
+// As swiglus, with gelu: past z = -87 with exp(z / 2) twice.
+template <int N>
+__device__ __forceinline__ void geglus(const float (&u)[N], const float (&v)[N], float (&o)[N]) {
+  float t[N], most = 0.0f;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < N; ++r) {
     t[r] = gelu_exponent(u[r], gelu_square(u[r]));
     most = fmaxf(most, t[r]);
   }
   if (__any(most > 125.0f)) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
+    for (int r = 0; r < N; ++r) {
       const float h = __builtin_amdgcn_exp2f(t[r] * -0.5f);
       o[r] = t[r] > 125.0f ? u[r] * h * v[r] * h : u[r] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t[r])) * v[r];
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[r] = u[r] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t[r])) * v[r];
+    for (int r = 0; r < N; ++r) o[r] = u[r] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t[r])) * v[r];
   }
 }
 
@@ -106,7 +108,7 @@ __device__ __forceinline__ void gate_back_far(float t, float dh, float& u, float
   v = a * dh * p;
   u = d;
 }
-// For eight of a lane's values; as in swiglu16 the far form only where a lane of
+// For eight of a lane's values; as in swiglus the far form only where a lane of
 // the wave needs it, and each value by its own gate.
 template <bool GELU>
 __device__ __forceinline__ void gate_back8(const float (&dh)[8], float (&u)[8], float (&v)[8], float (&h)[8]) {

@@ -51,7 +51,8 @@ int forward_plan(const gmmgf_args* a, Plan* pl) {
   product.activation = GMMGM_ACT_SWIGLU;  // a gate of its columns' first half
   product.tuning_config = a->tuning_config;
   product.tuning_config_len = a->tuning_config_len;
-  const int st = product_plan(&product, pl);
+  // (a scale's 32 columns are one tile's: none thinner where they are kept in FP8)
+  const int st = product_plan(&product, pl, !given(a->kept) || a->kept.dtype != GMMFR_DT_FLOAT8_E4M3FN);
   if (st != GMMFR_OK) return st;
   pl->p.act = a->activation;
   pl->p.hidden = nullptr;

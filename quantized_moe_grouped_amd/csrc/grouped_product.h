@@ -297,7 +297,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int NS = BK / KSLICE;       // slices of a stage
   constexpr int MY_M = KWAVES ? 1 : WM, MY_N = KWAVES ? 1 : WN;  // waves across the tile
   constexpr int WTM = BM / MY_M, WTN = BN / MY_N, FM = WTM / 32, FN = WTN / 32;
-  static_assert(FM >= 1 && FN >= 1 && FM * 32 * MY_M == BM && FN * 32 * MY_N == BN && (!GLU || FN % 2 == 0), "tile");
+  static_assert(FM >= 1 && FN >= 1 && FM * 32 * MY_M == BM && FN * 32 * MY_N == BN && (!GLU || FN % 2 == 0 || (FORM == kGated && BN == 32)), "tile");
+  // columns of a block that are gates, and the ups behind them: blocks of either, or half and half
+  constexpr int GC = GLU && BN == 32 ? 16 : 32;
   static_assert(!(KWAVES && WGRAD), "the narrow tile has the same steps everywhere");
   static_assert(FORM == kStore || (!MX && !WGRAD && GLU == (FORM == kGated)), "gated forms");
   static_assert(KWAVES ? NS == NWAVES : NS == 2 || NS == 4, "one slice of a stage for each wave, or two or four");
@@ -426,8 +428,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // column of the weights for column q of the tile; -1 past the last
   auto column = [&](const Tile& c, int q) -> int {
     if constexpr (GLU) {
-      const int f = c.n0 + (q >> 6) * 32 + (q & 31);
-      return f < F ? f + ((q & 32) ? (int)F : 0) : -1;
+      const int f = c.n0 + q / (2 * GC) * GC + q % GC;
+      return f < F ? f + ((q & GC) ? (int)F : 0) : -1;
     } else {
       return c.n0 + q < p.n ? c.n0 + q : -1;
     }
@@ -951,8 +953,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       store_16<ENC == kF16>(kept + F, n, width, lane, v);
     }
     float o[16];
-    if (p.act == GMMGF_ACT_GEGLU) geglu16(u, v, o);
-    else swiglu16(u, v, o);
+    if (p.act == GMMGF_ACT_GEGLU) geglus(u, v, o);
+    else swiglus(u, v, o);
     store_16<ENC == kF16>((uint16_t*)p.y + at * F, n, width, lane, o);
   };
   // One block of the way back; `k`: what was kept for it.
@@ -1003,6 +1005,24 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // The same for a block that is half gates, half ups: a lane's first eight
+  // values and its last eight, sixteen columns of h.
+  auto gated_half = [&](const Tile& c, int lane, const v16f& sums) {
+    const int row = lane & 31;
+    if (row >= c.valid) return;
+    const int64_t at = c.m0 + row;
+    float u[8], v[8], o[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) u[r] = sums[r], v[r] = sums[8 + r];
+    if (p.keep == kKeepFull) {
+      uint16_t* kept = (uint16_t*)p.kept + at * 2 * F;
+      store_piece<ENC == kF16>(kept, c.n0, (int)F, lane, 0, u);
+      store_piece<ENC == kF16>(kept + F, c.n0, (int)F, lane, 0, v);
+    }
+    if (p.act == GMMGF_ACT_GEGLU) geglus(u, v, o);
+    else swiglus(u, v, o);
+    store_piece<ENC == kF16>((uint16_t*)p.y + at * F, c.n0, (int)F, lane, 0, o);
+  };
   auto epilogue = [&](const Tile& c) {
     int lane = threadIdx.x & 63;  // opaque, as in set_sources
     asm volatile("" : "+v"(lane));
@@ -1039,6 +1059,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       }
       return;
     }
+    if constexpr (GLU && BN == 32) {
+      gated_half(c, lane, acc[0][0]);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if constexpr (GLU) {
@@ -1050,7 +1074,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           if constexpr (FORM == kGated) {
             gated_block(c, lane, i, (wn * WTN + j * 32) / 2, u, v);
           } else {
-            swiglu16(u, v, v);
+            swiglus(u, v, v);
             store_block(c, lane, i, (wn * WTN + j * 32) / 2, v);
           }
         }
@@ -1345,8 +1369,8 @@ inline int aligned(std::initializer_list<const gmmfr_tensor*> all) {
   return GMMFR_OK;
 }
 
-enum Kind { kLarge = 0, kMiddle = 1, kSmall = 2 };
-constexpr int kTileM[3] = {256, 128, 32}, kTileN[3] = {256, 128, 64}, kPerCu[3] = {1, 2, 2};
+enum Kind { kLarge = 0, kMiddle = 1, kSmall = 2, kThin = 3 };
+constexpr int kTileM[4] = {256, 128, 32, 32}, kTileN[4] = {256, 128, 64, 32}, kPerCu[4] = {1, 2, 2, 2};
 
 struct Plan {
   Params p;
@@ -1391,7 +1415,7 @@ inline int grid_of(const Plan& pl, int64_t tiles, int64_t cap) {
   return (int)(g < 1 ? 1 : g);
 }
 
-inline int product_plan(const gmmgm_args* a, Plan* pl) {
+inline int product_plan(const gmmgm_args* a, Plan* pl, bool thin_gate = false) {
   if (!a) return GMMFR_ERR_NULLPTR;
   if (!given(a->x) || !given(a->w) || !given(a->group_list) || !given(a->y)) return GMMFR_ERR_NULLPTR;
   const int xt = a->x.dtype, wt = a->w.dtype, yt = a->y.dtype;
@@ -1492,11 +1516,21 @@ inline int product_plan(const gmmgm_args* a, Plan* pl) {
   };
   pl->kind = height ? (height == 256 ? kLarge : height == 128 ? kMiddle : kSmall)
                     : (narrow ? kSmall : larger_kind(along(256), along(128), n, mx));
-  const int tn = glu ? kTileN[pl->kind] / 2 : kTileN[pl->kind];
+  auto tiles_of = [&](Kind kind) -> int64_t {
+    p.tiles_n = (int32_t)ceil_div(n, kTileN[kind]);
+    // at most this many tiles: whole ones, and one part a non-empty expert
+    return (m / kTileM[kind] + parts) * p.tiles_n;
+  };
   p.tiles_m = 0;
-  p.tiles_n = (int32_t)ceil_div(glu ? n / 2 : n, tn);
-  // at most this many tiles: whole ones, and one part a non-empty expert
-  const int64_t tiles = (m / kTileM[pl->kind] + parts) * p.tiles_n;
+  int64_t tiles = tiles_of(pl->kind);
+  // Narrow tiles that leave CUs without one: a CU streams weights at 27 GB/s
+  // whatever is in flight (stages twice as deep, or twice as long: slower), so
+  // they are cut in two for twice as many.  Weights (e,n,k) of 16 bits only:
+  // those of (e,k,n) would be read half a line at a time, and the scales of
+  // microscaled ones are staged for 64 columns.  us, 64 columns against 32:
+  //   7168 x 4096, 1 row    64 tiles  34, 24    16384 x 8192      128  74, 59
+  //   8 of 2048 x 1024     128        14, 11    16 of 2048 x 1024 256  18, 18
+  if (pl->kind == kSmall && !mx && (!glu || thin_gate) && !pl->col && tiles <= 256) tiles = tiles_of(pl->kind = kThin);
   if (tiles >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
   pl->grid = grid_of(*pl, tiles, cap);
   return GMMFR_OK;
@@ -1570,6 +1604,11 @@ hipError_t launch(Plan& pl, hipStream_t s) {
                                                        FOUR ? 2 : 4, 2, WGRAD ? 4 : 2, false, FOUR ? 1 : 2, FORM>,
                            dim3(pl.grid), dim3(FOUR ? 256 : 512), args, dyn, s);
   if constexpr (!WGRAD) {
+    if constexpr ((ENC == kBf16 || ENC == kF16) && !WCOL && (!GLU || FORM == kGated)) {
+      if (pl.kind == kThin)
+        return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 32, BK, 2, 2, STS, true, 2, FORM>,
+                               dim3(pl.grid), dim3(256), args, dyn, s);
+    }
     if (pl.kind == kSmall)
       return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 32, 64, BKS, 2, 2, STS, true, 2, FORM>,
                              dim3(pl.grid), dim3(256), args, dyn, s);

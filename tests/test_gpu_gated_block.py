@@ -159,6 +159,38 @@ def test_tiles_agree():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("m,e,k,f,tiles", [(20, 3, 200, 328, "thin"), (40, 5, 136, 1000, "thin"), (1, 1, 2048, 4096, "thin"),
+                                           (9, 2, 72, 8, "thin"), (33, 16, 64, 640, "thin"), (40, 24, 136, 1000, "narrow"),
+                                           (33, 16, 64, 1600, "narrow")])
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+def test_narrow_tiles_of_both_widths(m, e, k, f, tiles, act):
+    """Weights (e,n,k) under few tiles (32 columns each, a gate's and its up's in
+    one block) and under more (64)."""
+    rng = np.random.default_rng(f)
+    counts = R.counts_for(rng, m, e, 0.2)
+    gl = torch.from_numpy(counts).cuda()
+    x, w1, w2 = _rand(rng, (m, k)), _rand(rng, (e, 2 * f, k), scale=1.5 * k ** -0.5), _rand(rng, (e, f, k), scale=k ** -0.5)
+    kw = dict(activation=act, transpose_w=True, group_list_type=1, tuning_config=[0, 32])
+    info = B.GmPlanInfo()
+    dh = torch.empty((m, f), dtype=BF16, device="cuda")
+    args, keepalive = B.make_gm_args(x.cuda(), w2.cuda(), gl, dh, transpose_w=True, group_list_type=1, tuning_config=[0, 32])
+    assert B.lib().gmm_grouped_matmul_plan(ctypes.byref(args), ctypes.byref(info)) == B.OK
+    assert info.tile_n == (32 if tiles == "thin" else 64)
+    both, s = R.product(x.double(), w1.double().transpose(1, 2), counts, 1)
+    want, bound = G.forward(both, s * (k + 1) * R.U, act)
+    h, kept, _ = B.gated_matmul(x.cuda(), w1.cuda(), gl, keep="full", **kw)
+    _check(h, want, bound, "h")
+    _check(kept, both, s * (k + 1) * R.U, "kept")
+    assert torch.equal(B.gated_matmul(x.cuda(), w1.cuda(), gl, **kw)[0], h)
+    if f % 32 == 0:  # kept in FP8 the tiles are wider; the sums are the same
+        assert torch.equal(B.gated_matmul(x.cuda(), w1.cuda(), gl, keep="fp8", **kw)[0], h)
+    dh, s = R.product(x.double(), w2.double().transpose(1, 2), counts, 1)
+    want, bound, h_want, h_bound = G.backward(dh, s * (k + 1) * R.U, kept.cpu().double(), act)
+    d, hb = B.gated_matmul_backward(x.cuda(), w2.cuda(), gl, kept, **kw)
+    _check(d, want, bound, "gradients")
+    _check(hb, h_want, h_bound, "h again")
+
+
 def _calls():
     """Calls on inputs of their own (1 MiB or more each: blocks of their own)."""
     gl = torch.tensor([512, 1024], device="cuda")
