@@ -9,6 +9,10 @@
 // A lane holds 16 values of one row of a block: of row l % 32 the columns
 // 8 q + 4 h + r, q, r = 0..3, h = l / 32.  A register swap between the wave's
 // halves gives it neighbouring columns to store, and is its own inverse.
+//
+// The gate is two of the quarter-rate instructions (2^x, 1/x) and about six
+// others a value forward, ten backward; what its products leave of a tile's time
+// is the memory's (see gated_matmul.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 

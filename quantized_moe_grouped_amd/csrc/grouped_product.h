@@ -9,7 +9,9 @@
 // Operands are bf16 or fp16, or microscaled: FP8 E4M3 or FP4 E2M1 rows with
 // FP4 E2M1 weights and one E8M0 scale per 32 values along the reduction.
 // Sums run in fp32 on the matrix cores; the result is rounded once, on
-// storing.
+// storing.  The gated block's forms (gate.h, gated_matmul.hip) work on the sums
+// before that; the weight gradient takes one operand in FP8 with scales across
+// the reduction, too (wgrad_fp8.hip).
 //
 // One kernel template, product_kernel: C(M,N) += A(M,R) * B(R,N) over the
 // tiles of all experts.  In the product M is the group's rows, N the weight
@@ -30,13 +32,16 @@
 //     then holds four neighbouring columns of one row, and a swap of two
 //     registers between the wave's halves makes them eight, stored in 16
 //     bytes.
+//   - Fragments of the next slice are read between the present one's products
+//     (one after the other before them they hold the LDS, and the waves' issue:
+//     weight gradient 1133 -> 1097 us, the gated block 1815 -> 1787).
 //
 // What bounds it (one MI355X; rows over experts):
 //   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.90 to 0.95
 //     ms from box to box, 1.02 to 1.06 PFLOP/s.  Matrix cores busy 64% of the
 //     cycles at the 1.74 GHz that the card's power leaves; between them the
 //     waits for LDS and barriers.
-//   - weight gradient of the same: 1.11 ms, 45% busy at 1.92 GHz: one
+//   - weight gradient of the same: 1.10 ms, 45% busy at 1.92 GHz: one
 //     workgroup a CU (its sums fill the registers), whose 1.9 GB of fp32
 //     results go out ahead of copies that the next tile's first step waits for.
 //   - FP4, 131072 x 7168 x 4096 over 32, SwiGLU: 2.01 to 2.08 ms, 3.7 to 3.8
@@ -1204,7 +1209,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     // that follow the barrier and those of the next slice (all at once they
     // block the waves; later ones land too late: a quarter later cost 2-4%);
     // with two slices of microscaled operands, whose products take longer, all
-    // between the former.  The first fragments of a step are read before the
+    // between the former.  The first fragments of a step are read between the
     // last products of the one before.  Copies are issued under no condition
     // (past the last tile they copy zeros): the compiler would move the
     // products behind the branch.
