@@ -68,7 +68,8 @@ int forward_plan(const gmmgf_args* a, Plan* pl) {
   product.tuning_config = a->tuning_config;
   product.tuning_config_len = a->tuning_config_len;
   // (a scale's 32 columns are one tile's: none thinner where they are kept in FP8)
-  const int st = product_plan(&product, pl, !given(a->kept) || a->kept.dtype != GMMFR_DT_FLOAT8_E4M3FN);
+  const bool fp8 = given(a->kept) && a->kept.dtype == GMMFR_DT_FLOAT8_E4M3FN;
+  const int st = product_plan(&product, pl, kFewTiles | (fp8 ? 0 : kThinGate));
   if (st != GMMFR_OK) return st;
   pl->p.act = a->activation;
   pl->p.hidden = nullptr;
@@ -93,7 +94,7 @@ int backward_plan(const gmmgb_args* a, Plan* pl) {
   product.activation = GMMGM_ACT_NONE;
   product.tuning_config = a->tuning_config;
   product.tuning_config_len = a->tuning_config_len;
-  int st = product_plan(&product, pl);
+  int st = product_plan(&product, pl, kFewTiles);
   if (st != GMMFR_OK) return st;
   Params& p = pl->p;
   if (p.n > 32768) return GMMFR_ERR_SHAPE;  // 2 f, as in the forward pass

@@ -1420,7 +1420,9 @@ inline int grid_of(const Plan& pl, int64_t tiles, int64_t cap) {
   return (int)(g < 1 ? 1 : g);
 }
 
-inline int product_plan(const gmmgm_args* a, Plan* pl, bool thin_gate = false) {
+// What the gated forms' plans may take beside the plain product's.
+enum More { kThinGate = 1, kFewTiles = 2 };
+inline int product_plan(const gmmgm_args* a, Plan* pl, int more = 0) {
   if (!a) return GMMFR_ERR_NULLPTR;
   if (!given(a->x) || !given(a->w) || !given(a->group_list) || !given(a->y)) return GMMFR_ERR_NULLPTR;
   const int xt = a->x.dtype, wt = a->w.dtype, yt = a->y.dtype;
@@ -1509,8 +1511,18 @@ inline int product_plan(const gmmgm_args* a, Plan* pl, bool thin_gate = false) {
     if (ceil_div(m, rows) < busy) busy = ceil_div(m, rows);
   }
   const int64_t middle = busy * ceil_div(n, kTileN[kMiddle]);  // 128-row tiles, one row of them an expert
-  const bool narrow = avg <= 16 ? !pl->col || middle <= 256
-                                : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256));
+  // The gated forms take the narrow tiles too where all of them are one round of
+  // the chip, or two with weights (e,n,k): 128-row tiles leave most CUs idle then
+  // (us, narrow against 128-row, 16 bits kept, (e,n,k) and (e,k,n); forward):
+  //   1 of 7168 x 4096, 64 rows     128 tiles   26, 102    56,  99
+  //   8 of 7168 x 2048, 40 rows     512         43,  77    65,  74
+  //   6 of 6352 x 512, 269 rows     432         60,  92    60,  88
+  //   2 of 7168 x 4096, 256 rows   1024         77,  81    95,  79
+  // (way back, (e,f,d), the last two: 34, 97 and 45, 86).
+  const int64_t few = busy * ceil_div(avg, 32) * ceil_div(n, 64);
+  const bool narrow = ((more & kFewTiles) && few <= (pl->col ? 512 : 1024)) ||
+                      (avg <= 16 ? !pl->col || middle <= 256
+                                 : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256)));
   // One expert's rows are known but for those behind it: whole tiles of them
   // (4096 rows of 7168 bf16 (e,n,k), us under 128-row and 256-row tiles: n =
   // 4096 with a gate 218, 183, n = 2048 112, 135).
@@ -1535,7 +1547,7 @@ inline int product_plan(const gmmgm_args* a, Plan* pl, bool thin_gate = false) {
   // microscaled ones are staged for 64 columns.  us, 64 columns against 32:
   //   7168 x 4096, 1 row    64 tiles  34, 24    16384 x 8192      128  74, 59
   //   8 of 2048 x 1024     128        14, 11    16 of 2048 x 1024 256  18, 18
-  if (pl->kind == kSmall && !mx && (!glu || thin_gate) && !pl->col && tiles <= 256) tiles = tiles_of(pl->kind = kThin);
+  if (pl->kind == kSmall && !mx && (!glu || (more & kThinGate)) && !pl->col && tiles <= 256) tiles = tiles_of(pl->kind = kThin);
   if (tiles >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
   pl->grid = grid_of(*pl, tiles, cap);
   return GMMFR_OK;

@@ -144,19 +144,47 @@ def test_results_do_not_depend_on_the_grid(height):
 
 
 def test_tiles_agree():
-    """128-row and 256-row tiles add in one order; the expected rows choose between them."""
+    """128-row and 256-row tiles add in one order, whatever rows are expected."""
     rng = np.random.default_rng(14)
     m, e, k, f = 700, 4, 264, 96
     gl = R.as_list(R.counts_for(rng, m, e, 0.2), 1).cuda()
     x, w1, w2 = _rand(rng, (m, k)).cuda(), _rand(rng, (e, k, 2 * f), scale=0.1).cuda(), _rand(rng, (e, f, k), scale=0.1).cuda()
     got = []
-    for tuning in ([0, 128], [0, 256], [40], [700]):
+    for tuning in ([0, 128], [0, 256], [40, 128, 8], [700, 256]):
         kw = dict(group_list_type=1, tuning_config=tuning)
         h, kept, _ = B.gated_matmul(x, w1, gl, keep="full", **kw)
         got.append([h, kept, *B.gated_matmul_backward(x, w2, gl, kept, **kw)])
     for other in got[1:]:
         for a, b in zip(got[0], other):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,e,k,f", [(48, 1, 512, 1024), (269, 3, 392, 256), (200, 2, 136, 800), (512, 4, 128, 2048), (512, 4, 128, 2080), (130, 3, 64, 72)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_chosen_tiles(m, e, k, f, transpose):
+    """Few rows of small weights under the tile that the plan takes, on either
+    side of its bound: results of some tile's, forward and back."""
+    rng = np.random.default_rng(f + m)
+    counts = R.counts_for(rng, m, e, 0.2)
+    gl = torch.from_numpy(counts).cuda()
+    x = _rand(rng, (m, k))
+    w1 = _rand(rng, (e, 2 * f, k) if transpose else (e, k, 2 * f), scale=1.5 * k ** -0.5)
+    w2 = _rand(rng, (e, f, k) if transpose else (e, k, f), scale=k ** -0.5)
+    kw = dict(transpose_w=transpose, group_list_type=1)
+    h, kept, _ = B.gated_matmul(x.cuda(), w1.cuda(), gl, keep="full", **kw)
+    d, hb = B.gated_matmul_backward(x.cuda(), w2.cuda(), gl, kept, **kw)
+    fits = []
+    for height in (32, 128):
+        other, also, _ = B.gated_matmul(x.cuda(), w1.cuda(), gl, keep="full", tuning_config=[0, height], **kw)
+        fits.append(torch.equal(h, other) and torch.equal(kept, also))
+    assert any(fits)
+    both, s = R.product(x.double(), (w1.transpose(1, 2) if transpose else w1).double(), counts, 1)
+    want, bound = G.forward(both, s * (k + 1) * R.U, "swiglu")
+    _check(h, want, bound, "h")
+    dh, s = R.product(x.double(), (w2.transpose(1, 2) if transpose else w2).double(), counts, 1)
+    want, bound, h_want, h_bound = G.backward(dh, s * (k + 1) * R.U, kept.cpu().double(), "swiglu")
+    _check(d, want, bound, "gradients")
+    _check(hb, h_want, h_bound, "h again")
 
 
 @pytest.mark.parametrize("m,e,k,f,tiles", [(20, 3, 200, 328, "thin"), (40, 5, 136, 1000, "thin"), (1, 1, 2048, 4096, "thin"),
