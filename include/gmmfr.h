@@ -421,7 +421,9 @@ int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t wor
  * multiplied (gmm_mx_quantize), as x, or as dy for weights kept as (e,n,k).  A
  * value is its code times its block's scale, brought to the other operand's
  * type (exact in BFLOAT16, rounded to nearest in FLOAT16); the result is that
- * of gmm_grouped_matmul_wgrad on such values, to the bit.
+ * of gmm_grouped_matmul_wgrad on such values, to the bit, unless the plan splits
+ * the groups' rows (few tiles, 2048 rows an expert and more): then the parts'
+ * fp32 sums meet in the workspace, in one order whatever the launch.
  */
 typedef struct {
   gmmfr_tensor x;           /* (m,k): BFLOAT16 or FLOAT16, or FLOAT8_E4M3FN          required */
@@ -438,7 +440,9 @@ typedef struct {
 } gmmgx_args;
 
 /* Limits: those of gmm_grouped_matmul_wgrad, and 64 divides the columns of the
- * FLOAT8 operand.  Two stages as there. */
+ * FLOAT8 operand.  Two stages as there, but for the workspace: 0 bytes, or e k n
+ * FLOAT32 values for each part, 16-byte aligned; its contents need no
+ * initialisation.  Stage 2 returns GMMFR_ERR_WORKSPACE when it is too small. */
 int gmm_grouped_matmul_wgrad_fp8_workspace(const gmmgx_args* args, size_t* workspace_bytes);
 int gmm_grouped_matmul_wgrad_fp8(const gmmgx_args* args, void* workspace, size_t workspace_bytes, void* stream);
 

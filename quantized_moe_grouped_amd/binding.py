@@ -596,8 +596,8 @@ def _on(dev, stream, call, *args):
 
 
 def _enqueue(name: str, raw: bytes, workspace, handle) -> None:
-    """Stage 2.  These calls want no workspace (stage 1 says 0 bytes); one that
-    is given is passed on."""
+    """Stage 2.  These calls want no workspace (stage 1 says 0 bytes), but for the
+    weight gradient of FP8 rows, sometimes; one that is given is passed on."""
     ptr, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = getattr(lib(), name)(raw, ptr, size, handle)
     if st != OK:
@@ -643,7 +643,8 @@ def grouped_matmul_wgrad(x, dy, group_list, *, x_scale=None, dy_scale=None, out=
     accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x).
     One of the two may be in FP8 with its scales (x_scale or dy_scale, as
     mx_quantize makes them): the result is that of the same values in the other
-    operand's type.  With a gate dy is the gradient of the product before it
+    operand's type, but for the order of additions where the rows of few, long
+    groups are split (a workspace is allocated then, if none is given).  With a gate dy is the gradient of the product before it
     (gated_matmul_backward)."""
     dev = _check_tensors(x, dy, group_list, x_scale, dy_scale, out, workspace)
     if accumulate and out is None:
@@ -664,6 +665,13 @@ def _grouped_matmul_wgrad(handle, x, dy, group_list, x_scale, dy_scale, out, out
         _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
     else:
         raw = _gx_bytes(x, dy, x_scale, dy_scale, group_list, out, group_list_type, accumulate, tail)
+        if workspace is None and x.shape[0] >= 2048 * group_list.shape[0]:  # else none is wanted
+            need = ctypes.c_size_t(0)
+            st = lib().gmm_grouped_matmul_wgrad_fp8_workspace(raw, ctypes.byref(need))
+            if st != OK:
+                raise GmmfrError(st, "gmm_grouped_matmul_wgrad_fp8")
+            if need.value:
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
         _enqueue("gmm_grouped_matmul_wgrad_fp8", raw, workspace, handle)
     del tuning
     return out

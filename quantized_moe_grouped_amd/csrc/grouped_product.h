@@ -108,6 +108,7 @@ struct Params {
   uint8_t* kept_scale;       // E8M0 (m, 2 n'/32) where it is kept in FP8
   void* hidden;
   int32_t keep, act;
+  int32_t splits;            // weight gradient of FP8 rows: parts of every group's rows
 };
 
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
@@ -264,6 +265,7 @@ struct Tile {
   int n0;      // first column (SwiGLU: of y)
   int r0, r1;  // the reduction's range (wgrad: the group's rows)
   bool alone;  // the group has no other tile along M
+  int part;    // of the group's rows (weight gradient of FP8 rows)
 };
 
 template <int N, int I = 0, typename F>
@@ -366,7 +368,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const int wm = KWAVES ? 0 : wave / WN, wn = KWAVES ? 0 : wave % WN;
   group_table(p, WGRAD ? 1 : BM, s_ends, s_pre);
   if constexpr (WGRAD) length_order(p, s_ends, s_pre);  // the tiles' numbers need no table here
-  const int total = WGRAD ? p.e * p.tiles_m * p.tiles_n : s_pre[p.e];
+  const int parts = EIGHT != kNone8 ? p.splits : 1;
+  const int total = WGRAD ? p.e * parts * p.tiles_m * p.tiles_n : s_pre[p.e];
   const int64_t F = GLU ? p.n / 2 : p.n;  // columns of y
   const int64_t x_row = WGRAD ? p.k * (X8 ? 1 : 2) : p.k * XBITS / 8;  // bytes
   const int64_t w_row = WCOL ? p.n * (W8 ? 1 : 2) : p.k * WBITS / 8;
@@ -395,7 +398,15 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     int local, mtiles;
     if constexpr (WGRAD) {
       const int n = t / (p.tiles_m * p.tiles_n);
-      c.g = __builtin_amdgcn_readfirstlane(s_pre[n]);
+      int at = n;
+      c.part = 0;
+      if constexpr (EIGHT != kNone8) {
+        if (parts > 1) {
+          at = n / parts;
+          c.part = n - at * parts;
+        }
+      }
+      c.g = __builtin_amdgcn_readfirstlane(s_pre[at]);
       local = t - n * p.tiles_m * p.tiles_n;
       mtiles = p.tiles_m;
     } else {
@@ -422,6 +433,13 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     c.n0 = nt * (GLU ? BN / 2 : BN);
     c.r0 = WGRAD ? begin : 0;
     c.r1 = WGRAD ? end : (int)p.k;
+    if constexpr (EIGHT != kNone8) {
+      if (parts > 1) {  // parts of whole steps
+        const int64_t len = ((uint32_t)(end - begin) / parts + BK) / BK * BK;
+        c.r0 = (int)min(begin + c.part * len, (int64_t)end);
+        c.r1 = (int)min(c.r0 + len, (int64_t)end);
+      }
+    }
     c.alone = mtiles == 1;
     return c;
   };
@@ -904,7 +922,8 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   auto store_block = [&](const Tile& c, int lane, int i, int col, const float (&v)[16]) {
     const int h = lane >> 5, row = wm * WTM + i * 32 + (lane & 31);
     if (row >= c.valid) return;
-    const int64_t at = (WGRAD ? (int64_t)c.g * p.k * p.n : 0) + (int64_t)(c.m0 + row) * F;
+    const int64_t g = EIGHT != kNone8 ? (int64_t)c.part * p.e + c.g : (int64_t)c.g;
+    const int64_t at = (WGRAD ? g * p.k * p.n : 0) + (int64_t)(c.m0 + row) * F;
     if (p.out == kOutF32) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

@@ -7,9 +7,10 @@
 // take (theirs lie along it), so codes become 16-bit values on their way: they
 // are copied to LDS as they are, half the bytes, and the thread that copied
 // sixteen of a row turns them into 16-bit values (one instruction for two, exact
-// in bf16), two steps before the matrix core has them.  In fp16, values past
+// in bf16), a step before the matrix core has them.  In fp16, values past
 // 65504 become infinite and those below 2^-14 lose bits.  The sums are those of
-// the 16-bit weight gradient on the widened rows, to the bit.
+// the 16-bit weight gradient on the widened rows, to the bit, where the groups'
+// rows are not split.
 //
 // 32768 rows over 32 experts, 7168 x 4096, fp32 results (one MI355X): 2.26 to
 // 2.32 ms, 0.83 to 0.85 PFLOP/s, the 16-bit gradient of the same rows 2.24,
@@ -21,7 +22,47 @@
 
 namespace gmmgm {
 
-int wgrad_fp8_plan(const gmmgx_args* a, Plan* pl, bool* x8) {
+// Where the tiles leave workgroups without one and groups are long, the rows of
+// each are split into parts of 1024 and more: their sums go to a workspace, one
+// after the other in memory, and sum_parts adds them in their order.  256-row
+// tiles if their parts fill three quarters of the chip (us, whole, and split with
+// 128-row and 256-row tiles; fp32 results):
+//   1 of 1024 x 1024, 16384 rows  248,  59,  55    1 of 512 x 512, 8192 rows  124, 30, 46
+//   2 of 832 x 864, 25694         198,  69,  66    4 of 512 x 512, 16384       65, 31, 47
+//   1 of 2048 x 2048, 16384       240, 179, 140    1 of 128 x 128, 4096        64, 25, 39
+int parts_of(const Params& p, Kind kind) {
+  const int64_t tiles = p.e * ceil_div(p.k, kTileM[kind]) * ceil_div(p.n, kTileN[kind]);
+  int64_t parts = 256 * kPerCu[kind] / tiles;
+  if (parts > p.m / p.e / 1024) parts = p.m / p.e / 1024;
+  if (parts > 16) parts = 16;
+  return parts < 2 ? 1 : (int)parts;
+}
+
+typedef float sum4 __attribute__((ext_vector_type(4)));
+__global__ __launch_bounds__(256) void sum_parts(const sum4* parts, void* dw, int64_t fours, int splits, int out, int accumulate) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < fours; i += (int64_t)gridDim.x * 256) {
+    sum4 v = parts[i];
+    for (int s = 1; s < splits; ++s) {
+      const sum4 o = parts[s * fours + i];
+      v = sum4{v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w};
+    }
+    if (out == kOutF32) {
+      if (accumulate) {
+        const sum4 o = ((const sum4*)dw)[i];
+        v = sum4{v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w};
+      }
+      ((sum4*)dw)[i] = v;
+    } else if (out == kOutF16) {
+      typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+      ((v4h*)dw)[i] = v4h{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+    } else {
+      typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+      ((v4bf*)dw)[i] = v4bf{(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w};
+    }
+  }
+}
+
+int wgrad_fp8_plan(const gmmgx_args* a, Plan* pl, bool* x8, size_t* workspace) {
   if (!a) return GMMFR_ERR_NULLPTR;
   if (!given(a->x) || !given(a->dy) || !given(a->group_list) || !given(a->dw)) return GMMFR_ERR_NULLPTR;
   *x8 = a->x.dtype == GMMFR_DT_FLOAT8_E4M3FN;
@@ -47,6 +88,18 @@ int wgrad_fp8_plan(const gmmgx_args* a, Plan* pl, bool* x8) {
   if (columns % 64 != 0 || !shape_is(scale, 3, pl->p.m, columns / 64, 2)) return GMMFR_ERR_SHAPE;
   if (aligned({&scale}) != GMMFR_OK) return GMMFR_ERR_ALIGN;
   (*x8 ? pl->p.xs : pl->p.ws) = (const uint8_t*)scale.data;
+  Params& p = pl->p;
+  int64_t expected, height, cap;
+  tuning(a->tuning_config, a->tuning_config_len, &expected, &height, &cap);
+  if (height == 0) {
+    const int parts = parts_of(p, kLarge);
+    if (parts > 1 && parts * p.e * ceil_div(p.k, 256) * ceil_div(p.n, 256) >= 192) pl->kind = kLarge;
+    p.tiles_m = (int32_t)ceil_div(p.k, kTileM[pl->kind]);
+    p.tiles_n = (int32_t)ceil_div(p.n, kTileN[pl->kind]);
+  }
+  p.splits = parts_of(p, pl->kind);
+  pl->grid = grid_of(*pl, (int64_t)p.e * p.splits * p.tiles_m * p.tiles_n, cap);
+  *workspace = p.splits > 1 ? (size_t)p.splits * p.e * p.k * p.n * 4 : 0;
   return GMMFR_OK;
 }
 
@@ -61,6 +114,12 @@ hipError_t launch_fp8(Plan& pl, hipStream_t s) {
   return hipLaunchKernel(kernel, dim3(pl.grid), dim3(256), args, (size_t)(2 * pl.p.e + 1) * 4, s);
 }
 
+int launch_parts(Plan& pl, bool x8, hipStream_t s) {
+  const hipError_t done = pl.enc == kBf16 ? (x8 ? launch_fp8<kBf16, kX8>(pl, s) : launch_fp8<kBf16, kW8>(pl, s))
+                                          : (x8 ? launch_fp8<kF16, kX8>(pl, s) : launch_fp8<kF16, kW8>(pl, s));
+  return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+}
+
 }  // namespace gmmgm
 
 extern "C" {
@@ -70,24 +129,38 @@ using namespace gmmgm;
 int gmm_grouped_matmul_wgrad_fp8_workspace(const gmmgx_args* args, size_t* workspace_bytes) {
   Plan pl;
   bool x8;
-  const int st = wgrad_fp8_plan(args, &pl, &x8);
+  size_t need;
+  const int st = wgrad_fp8_plan(args, &pl, &x8, &need);
   if (st != GMMFR_OK) return st;
   if (!workspace_bytes) return GMMFR_ERR_NULLPTR;
-  *workspace_bytes = 0;
+  *workspace_bytes = need;
   return GMMFR_OK;
 }
 
 int gmm_grouped_matmul_wgrad_fp8(const gmmgx_args* args, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   Plan pl;
   bool x8;
-  const int st = wgrad_fp8_plan(args, &pl, &x8);
+  size_t need;
+  int st = wgrad_fp8_plan(args, &pl, &x8, &need);
   if (st != GMMFR_OK) return st;
   hipStream_t s = (hipStream_t)stream;
-  const hipError_t done = pl.enc == kBf16 ? (x8 ? launch_fp8<kBf16, kX8>(pl, s) : launch_fp8<kBf16, kW8>(pl, s))
-                                          : (x8 ? launch_fp8<kF16, kX8>(pl, s) : launch_fp8<kF16, kW8>(pl, s));
-  return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
+  Params& p = pl.p;
+  if (need == 0) return launch_parts(pl, x8, s);
+  if (!workspace || workspace_bytes < need) return GMMFR_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 15u) != 0) return GMMFR_ERR_ALIGN;
+  void* dw = p.y;
+  int out = p.out, accumulate = p.accumulate, splits = p.splits;
+  p.y = workspace;
+  p.out = kOutF32;
+  p.accumulate = 0;
+  st = launch_parts(pl, x8, s);
+  if (st != GMMFR_OK) return st;
+  int64_t fours = (int64_t)p.e * p.k * p.n / 4;
+  void* kargs[] = {&workspace, &dw, &fours, &splits, &out, &accumulate};
+  const int64_t groups = ceil_div(fours, 256);
+  return hipLaunchKernel((const void*)sum_parts, dim3((uint32_t)(groups < 2048 ? groups : 2048)), dim3(256), kargs, 0, s) == hipSuccess
+             ? GMMFR_OK
+             : GMMFR_ERR_HIP;
 }
 
 }  // extern "C"

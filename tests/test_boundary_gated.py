@@ -190,3 +190,19 @@ def test_one_experts_rows_are_whole_tiles(n, tile):
     with 2048 half a round, where 128-row tiles make a whole one."""
     for rows in ([], [4096], [0]):
         assert B.gm_plan(gm(m=4096, k=7168, n=n, e=1, **(dict(tuning=rows) if rows else {})))["tile_m"] == tile
+
+
+@pytest.mark.parametrize("sizes,parts", [
+    (dict(m=2047, k=128, n=128, e=1), 0), (dict(m=2048, k=128, n=128, e=1), 2), (dict(m=40000, k=128, n=128, e=1), 16),
+    (dict(m=40000, k=128, n=128, e=20), 0), (dict(m=40960, k=1024, n=4096, e=1), 4), (dict(m=40960, k=2048, n=4096, e=1), 2), (dict(m=40960, k=4096, n=4096, e=1), 0),
+])
+def test_wgrad_fp8_workspace(sizes, parts):
+    """Long groups under few tiles are split: a workspace of fp32 results a part."""
+    a = gx(**sizes)
+    need = parts * 4 * sizes["e"] * sizes["k"] * sizes["n"]
+    assert stage_one("gmm_grouped_matmul_wgrad_fp8", a) == (B.OK, need)
+    if need:  # refused before any launch
+        call = B.lib().gmm_grouped_matmul_wgrad_fp8
+        assert call(ctypes.byref(a), None, 0, None) == B.ERR_WORKSPACE
+        assert call(ctypes.byref(a), ctypes.c_void_p(0x10000), need - 1, None) == B.ERR_WORKSPACE
+        assert call(ctypes.byref(a), ctypes.c_void_p(0x10008), need, None) == B.ERR_ALIGN
