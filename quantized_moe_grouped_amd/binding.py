@@ -552,19 +552,25 @@ def make_mq_args(x, codes, scales, *, transpose: bool = False):
 
 def _check_tensors(x, *others):
     """The device of x.  No tensor may want a gradient that these calls would
-    lose (they record no history), and all live on one GPU, where the kernels
-    dereference their pointers."""
+    lose (they record no history), nor carry a tangent of forward-mode
+    differentiation (they read the values alone), and all live on one GPU,
+    where the kernels dereference their pointers."""
+    import torch
     dev, wanting, elsewhere = x.device, x.requires_grad, None
     for t in others:
         if t is not None:
             wanting = wanting or t.requires_grad
             if t.device != dev:
                 elsewhere = t.device
-    if wanting:
-        import torch
-        if torch.is_grad_enabled():
-            raise ValueError("these calls record no gradients: detach the tensors, or call them under torch.no_grad() or "
-                             "in a torch.autograd.Function of your own")
+    if wanting and torch.is_grad_enabled():
+        raise ValueError("these calls record no gradients: detach the tensors, or call them under torch.no_grad() or "
+                         "in a torch.autograd.Function of your own")
+    dual = torch.autograd.forward_ad
+    if dual._current_level >= 0:  # (none outside of a dual level; looked up for each tensor it would cost 2 us a call)
+        for t in (x, *others):
+            if t is not None and dual.unpack_dual(t).tangent is not None:
+                raise ValueError("these calls carry no tangents of forward-mode differentiation: unpack the tensors, or "
+                                 "call them in a torch.autograd.Function with a jvp of your own")
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {dev}")
     if elsewhere is not None:
