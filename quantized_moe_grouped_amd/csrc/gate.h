@@ -66,6 +66,12 @@ __device__ __forceinline__ float gelu_square(float u) { return fminf(u * u, 256.
 __device__ __forceinline__ float gelu_exponent(float u, float square) {  // -z log2(e)
   return u * __builtin_fmaf(square, -kGeluLog2 * kGeluCube, -kGeluLog2);
 }
+// z'(u), up to 56.  u z' meets s (1 - s), which is 0 past |u| = 16, so that u
+// goes no further than 16 there: beyond 6e36 the product would be infinite, and
+// with that 0 no number.  (An infinite gate's du is the limit, dh v or 0.)
+__device__ __forceinline__ float gelu_slope(float u) {
+  return __builtin_fmaf(gelu_square(u), 3.0f * kGelu * kGeluCube, kGelu);
+}
 // As swiglus, with gelu: past z = -87 with exp(z / 2) twice.
 template <int N>
 __device__ __forceinline__ void geglus(const float (&u)[N], const float (&v)[N], float (&o)[N]) {
@@ -95,7 +101,7 @@ template <bool GELU>
 __device__ __forceinline__ void gate_back(float t, float dh, float& u, float& v, float& h) {
   const float e = __builtin_amdgcn_exp2f(t), s = __builtin_amdgcn_rcpf(1.0f + e), a = u * s;
   float b = a;
-  if constexpr (GELU) b *= __builtin_fmaf(gelu_square(u), 3.0f * kGelu * kGeluCube, kGelu);
+  if constexpr (GELU) b = fminf(a, 16.0f) * gelu_slope(u);
   const float d = dh * v * __builtin_fmaf(b, e * s, s);
   h = a * v;
   v = dh * a;
@@ -106,7 +112,7 @@ template <bool GELU>
 __device__ __forceinline__ void gate_back_far(float t, float dh, float& u, float& v, float& h) {
   const float p = __builtin_amdgcn_exp2f(t * -0.5f), a = u * p;
   float b = u;
-  if constexpr (GELU) b *= __builtin_fmaf(gelu_square(u), 3.0f * kGelu * kGeluCube, kGelu);
+  if constexpr (GELU) b = fmaxf(u, -16.0f) * gelu_slope(u);
   const float d = dh * v * p * (1.0f + b) * p;
   h = a * v * p;
   v = a * dh * p;

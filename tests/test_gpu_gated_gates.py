@@ -102,3 +102,33 @@ def test_backward(keep, dtype, height, act):
         want, bound, h_want, h_bound = _backward(torch.full((m, f), dh, dtype=torch.float64), u, v, act)
         _check(d, want, bound, f"gradients, dh = {dh}")
         _check(h, h_want, h_bound, f"h again, dh = {dh}")
+
+
+HUGE = [6e36, 6.2e36, 1e37, 1e38, 3.3e38]  # z' u passes fp32's range from 6.1e36 on
+
+
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("height", [32, 128, 256])
+@pytest.mark.parametrize("keep", ["full", "fp8"])
+def test_gates_up_to_the_largest(keep, height, act):
+    """du is dh v behind a large positive gate, 0 behind a large negative one."""
+    g = _gates(BF16, [*HUGE, 1.0])
+    if keep == "fp8":
+        g = g.repeat_interleave(32)
+    up = torch.tensor([1.0, -2.0 ** -14, 2.0 ** -20, 1.5]).to(BF16)
+    m, f = len(up), len(g)
+    both = torch.cat((g.expand(m, f), up[:, None].expand(m, f)), 1).contiguous()
+    x, w = torch.zeros((m, 8), dtype=BF16), torch.zeros((1, 8, 2 * f), dtype=BF16)
+    x[:, :m], w[0, :m] = torch.eye(m, dtype=BF16), both
+    gl, tuning = torch.tensor([m]).cuda(), [0, height]
+    h, kept, scale = B.gated_matmul(x.cuda(), w.cuda(), gl, keep=keep, activation=act, tuning_config=tuning)
+    u, v = both.double().chunk(2, 1)
+    _check(h, *_forward(u, v, act), "h")
+    u, v = (kept.cpu().double() if scale is None else R.decode(kept.cpu(), scale.cpu())).chunk(2, 1)
+    dy = torch.zeros((m, 8), dtype=BF16, device="cuda")
+    dy[:, 0] = 2.0 ** -3
+    d, h = B.gated_matmul_backward(dy, torch.ones((1, f, 8), dtype=BF16, device="cuda"), gl, kept, kept_scale=scale, activation=act,
+                                   tuning_config=tuning)
+    want, bound, h_want, h_bound = _backward(torch.full((m, f), 2.0 ** -3, dtype=torch.float64), u, v, act)
+    _check(d, want, bound, "gradients")
+    _check(h, h_want, h_bound, "h again")
