@@ -414,6 +414,7 @@ typedef struct {
 
 /* Limits: those of gmm_grouped_matmul's 16-bit operands.  Two stages as there. */
 int gmm_grouped_matmul_wgrad_workspace(const gmmgw_args* args, size_t* workspace_bytes);
+int gmm_grouped_matmul_wgrad_plan(const gmmgw_args* args, gmmgm_plan_info* info); /* tiles of dw */
 int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -444,6 +445,7 @@ typedef struct {
  * FLOAT32 values for each part, 16-byte aligned; its contents need no
  * initialisation.  Stage 2 returns GMMFR_ERR_WORKSPACE when it is too small. */
 int gmm_grouped_matmul_wgrad_fp8_workspace(const gmmgx_args* args, size_t* workspace_bytes);
+int gmm_grouped_matmul_wgrad_fp8_plan(const gmmgx_args* args, gmmgm_plan_info* info);
 int gmm_grouped_matmul_wgrad_fp8(const gmmgx_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -481,6 +483,7 @@ typedef struct {
 /* Limits and stages: those of gmm_grouped_matmul's 16-bit operands with SwiGLU
  * (n = 2f: f % 8 == 0).  Outputs must not overlap each other or an input. */
 int gmm_gated_matmul_workspace(const gmmgf_args* args, size_t* workspace_bytes);
+int gmm_gated_matmul_plan(const gmmgf_args* args, gmmgm_plan_info* info); /* columns: of w */
 int gmm_gated_matmul(const gmmgf_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -515,6 +518,7 @@ typedef struct {
 
 /* Limits and stages as gmm_gated_matmul's, with d in k's place. */
 int gmm_gated_matmul_backward_workspace(const gmmgb_args* args, size_t* workspace_bytes);
+int gmm_gated_matmul_backward_plan(const gmmgb_args* args, gmmgm_plan_info* info); /* columns: of h */
 int gmm_gated_matmul_backward(const gmmgb_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /*

@@ -30,7 +30,9 @@ EXPORTED = ("gmm_finalize_routing_workspace", "gmm_finalize_routing", "gmm_final
             "gmm_grouped_matmul_workspace", "gmm_grouped_matmul", "gmm_grouped_matmul_wgrad_workspace",
             "gmm_grouped_matmul_wgrad", "gmm_mx_quantize", "gmm_mx_dequantize", "gmm_grouped_matmul_plan",
             "gmm_gated_matmul_workspace", "gmm_gated_matmul", "gmm_gated_matmul_backward_workspace",
-            "gmm_gated_matmul_backward", "gmm_grouped_matmul_wgrad_fp8_workspace", "gmm_grouped_matmul_wgrad_fp8")
+            "gmm_gated_matmul_backward", "gmm_grouped_matmul_wgrad_fp8_workspace", "gmm_grouped_matmul_wgrad_fp8",
+            "gmm_grouped_matmul_wgrad_plan", "gmm_grouped_matmul_wgrad_fp8_plan", "gmm_gated_matmul_plan",
+            "gmm_gated_matmul_backward_plan")
 ACTIVATION = {None: 0, "none": 0, "swiglu": 1}
 GATE = {"swiglu": 1, "geglu": 2}  # of the gated block
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GMMFR_NOALLOC_SCRATCH_BYTES
@@ -114,6 +116,10 @@ class GbArgs(ctypes.Structure):
     ]
 
 
+_PLANS = {GmArgs: "gmm_grouped_matmul_plan", GwArgs: "gmm_grouped_matmul_wgrad_plan", GxArgs: "gmm_grouped_matmul_wgrad_fp8_plan",
+          GfArgs: "gmm_gated_matmul_plan", GbArgs: "gmm_gated_matmul_backward_plan"}
+
+
 class MqArgs(ctypes.Structure):
     _fields_ = [("x", Tensor), ("codes", Tensor), ("scales", Tensor), ("transpose", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
@@ -161,8 +167,8 @@ def lib():
             getattr(L, name + "_workspace").restype = ctypes.c_int
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
-        L.gmm_grouped_matmul_plan.argtypes = [ctypes.c_void_p, ctypes.POINTER(GmPlanInfo)]
-        L.gmm_grouped_matmul_plan.restype = ctypes.c_int
+            getattr(L, name + "_plan").argtypes = [ctypes.c_void_p, ctypes.POINTER(GmPlanInfo)]
+            getattr(L, name + "_plan").restype = ctypes.c_int
         for name in ("gmm_mx_quantize", "gmm_mx_dequantize"):
             getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
             getattr(L, name).restype = ctypes.c_int
@@ -504,12 +510,15 @@ def make_gm_args(x, w, group_list, y, *, x_scale=None, w_scale=None, group_list_
     return GmArgs.from_buffer_copy(raw), (x, w, group_list, y, x_scale, w_scale, tuning)
 
 
-def gm_plan(args: GmArgs) -> dict:
-    """The plan gmm_grouped_matmul takes for these arguments (host only)."""
+def gm_plan(args) -> dict:
+    """The plan that gmm_grouped_matmul, gmm_grouped_matmul_wgrad(_fp8),
+    gmm_gated_matmul or gmm_gated_matmul_backward takes, by the struct that the
+    arguments are (host only)."""
+    name = _PLANS[type(args)]
     info = GmPlanInfo()
-    st = lib().gmm_grouped_matmul_plan(ctypes.byref(args), ctypes.byref(info))
+    st = getattr(lib(), name)(ctypes.byref(args), ctypes.byref(info))
     if st != OK:
-        raise GmmfrError(st, "gmm_grouped_matmul_plan")
+        raise GmmfrError(st, name)
     return {"tile_m": info.tile_m, "tile_n": info.tile_n, "grid": info.grid}
 
 

@@ -134,6 +134,13 @@ int gmm_gated_matmul_workspace(const gmmgf_args* args, size_t* workspace_bytes) 
   return no_workspace(forward_plan(args, &pl), workspace_bytes);
 }
 
+int gmm_gated_matmul_plan(const gmmgf_args* args, gmmgm_plan_info* info) {
+  Plan pl;
+  const int st = describe(forward_plan(args, &pl), pl, info);
+  if (st == GMMFR_OK && pl.p.m == 0) info->grid = 0;
+  return st;
+}
+
 int gmm_gated_matmul(const gmmgf_args* args, void* workspace, size_t workspace_bytes, void* stream) {
   (void)workspace;
   (void)workspace_bytes;
@@ -145,6 +152,13 @@ int gmm_gated_matmul(const gmmgf_args* args, void* workspace, size_t workspace_b
 int gmm_gated_matmul_backward_workspace(const gmmgb_args* args, size_t* workspace_bytes) {
   Plan pl;
   return no_workspace(backward_plan(args, &pl), workspace_bytes);
+}
+
+int gmm_gated_matmul_backward_plan(const gmmgb_args* args, gmmgm_plan_info* info) {
+  Plan pl;
+  const int st = describe(backward_plan(args, &pl), pl, info);
+  if (st == GMMFR_OK && pl.p.m == 0) info->grid = 0;
+  return st;
 }
 
 int gmm_gated_matmul_backward(const gmmgb_args* args, void* workspace, size_t workspace_bytes, void* stream) {

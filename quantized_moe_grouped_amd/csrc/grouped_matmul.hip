@@ -43,13 +43,9 @@ using namespace gmmgm;
 
 int gmm_grouped_matmul_plan(const gmmgm_args* args, gmmgm_plan_info* info) {
   Plan pl;
-  const int st = product_plan(args, &pl);
-  if (st != GMMFR_OK) return st;
-  if (!info) return GMMFR_ERR_NULLPTR;
-  info->tile_m = kTileM[pl.kind];
-  info->tile_n = kTileN[pl.kind];
-  info->grid = pl.p.m == 0 ? 0 : pl.grid;
-  return GMMFR_OK;
+  const int st = describe(product_plan(args, &pl), pl, info);
+  if (st == GMMFR_OK && pl.p.m == 0) info->grid = 0;
+  return st;
 }
 
 int gmm_grouped_matmul_workspace(const gmmgm_args* args, size_t* workspace_bytes) {
@@ -74,6 +70,11 @@ int gmm_grouped_matmul_wgrad_workspace(const gmmgw_args* args, size_t* workspace
   if (!workspace_bytes) return GMMFR_ERR_NULLPTR;
   *workspace_bytes = 0;
   return GMMFR_OK;
+}
+
+int gmm_grouped_matmul_wgrad_plan(const gmmgw_args* args, gmmgm_plan_info* info) {
+  Plan pl;
+  return describe(wgrad_plan(args, &pl), pl, info);
 }
 
 int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t workspace_bytes, void* stream) {

@@ -1620,6 +1620,16 @@ inline int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   return GMMFR_OK;
 }
 
+// What the callers' plan queries give of a plan.
+inline int describe(int status, const Plan& pl, gmmgm_plan_info* info) {
+  if (status != GMMFR_OK) return status;
+  if (!info) return GMMFR_ERR_NULLPTR;
+  info->tile_m = kTileM[pl.kind];
+  info->tile_n = kTileN[pl.kind];
+  info->grid = pl.grid;
+  return GMMFR_OK;
+}
+
 // (hipLaunchKernel gives this launch's own status, where the runtime's last
 // error may be an earlier one of the program's)
 template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int FORM = kStore>

@@ -137,6 +137,13 @@ int gmm_grouped_matmul_wgrad_fp8_workspace(const gmmgx_args* args, size_t* works
   return GMMFR_OK;
 }
 
+int gmm_grouped_matmul_wgrad_fp8_plan(const gmmgx_args* args, gmmgm_plan_info* info) {
+  Plan pl;
+  bool x8;
+  size_t need;
+  return describe(wgrad_fp8_plan(args, &pl, &x8, &need), pl, info);
+}
+
 int gmm_grouped_matmul_wgrad_fp8(const gmmgx_args* args, void* workspace, size_t workspace_bytes, void* stream) {
   Plan pl;
   bool x8;
