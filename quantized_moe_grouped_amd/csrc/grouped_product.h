@@ -108,6 +108,7 @@ struct Params {
   uint8_t* kept_scale;       // E8M0 (m, 2 n'/32) where it is kept in FP8
   void* hidden;
   int32_t keep, act;
+  int32_t grid;              // workgroups (gridDim lies behind all this, a line of arguments more to fetch: 0.25 us)
   int32_t splits;            // weight gradient of FP8 rows: parts of every group's rows
 };
 
@@ -381,7 +382,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   // (with 64 of the 256-row tiles an XCD may have two rounds left where others
   // have none: FP8 ragged 638 -> 609 us, weight gradients 2-10%) and fewer
   // when there are few tiles, so that every XCD gets some
-  const int G = gridDim.x;
+  const int G = p.grid;
   const int block = max(1, min(BM >= 256 ? 32 : 64, (total + kXcds - 1) / kXcds));
   auto tile_at = [&](int j) -> int {
     int64_t t;
@@ -1664,3 +1665,4 @@ hipError_t launch(Plan& pl, hipStream_t s) {
 }
 
 }  // namespace gmmgm
+  pl.p.grid = pl.grid;

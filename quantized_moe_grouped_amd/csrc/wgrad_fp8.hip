@@ -107,6 +107,7 @@ int wgrad_fp8_plan(const gmmgx_args* a, Plan* pl, bool* x8, size_t* workspace) {
 // two operands' stages would not fit twice a CU beside the codes otherwise.
 template <int ENC, int EIGHT>
 hipError_t launch_fp8(Plan& pl, hipStream_t s) {
+  pl.p.grid = pl.grid;
   void* args[] = {&pl.p};
   const void* kernel = pl.kind == kLarge
                            ? (const void*)product_kernel<ENC, true, true, true, false, 256, 256, 32, 2, 2, 4, false, 1, kStore, EIGHT>
