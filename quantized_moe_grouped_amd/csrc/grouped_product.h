@@ -238,9 +238,11 @@ static __device__ void group_table(const Params& p, int bm, int32_t* s_ends, int
 
 // The experts whose groups are longer than twice the average first, the others
 // from the end: a weight gradient's tiles last as long as their group, and long
-// ones that began last would run alone (6007 rows, skewed over 48 of 1088 x
-// 1600, results of 16 bits: 121 -> 105 us).  One round of 64 experts a time, few instructions: every
-// workgroup does this before its first copy.
+// ones that began last would run alone (FP8 rows, 6007 of them skewed over 48 of
+// 1088 x 1600, results of 16 bits: 121 -> 105 us).  Not for rows of 16 bits: over
+// thirty skewed lists it took between 10% less and 13% more, and 2% more of even
+// ones.  One round of 64 experts a time, few instructions: every workgroup does
+// this before its first copy.
 static __device__ void length_order(const Params& p, const int32_t* s_ends, int32_t* s_order) {
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
@@ -368,7 +370,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = KWAVES ? 0 : wave / WN, wn = KWAVES ? 0 : wave % WN;
   group_table(p, WGRAD ? 1 : BM, s_ends, s_pre);
-  if constexpr (WGRAD) length_order(p, s_ends, s_pre);  // the tiles' numbers need no table here
   const int parts = EIGHT != kNone8 ? p.splits : 1;
   const int total = WGRAD ? p.e * parts * p.tiles_m * p.tiles_n : s_pre[p.e];
   const int64_t F = GLU ? p.n / 2 : p.n;  // columns of y
@@ -378,6 +379,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const bool s_split = MX && (s_row & 3) != 0;  // k % 128 == 64: odd rows' scales begin mid-dword
 
   // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
+  if constexpr (EIGHT != kNone8) length_order(p, s_ends, s_pre);  // the tiles' numbers need no table here
   // (workgroup b runs on XCD b % 8), as many a block as its 32 CUs run at once
   // (with 64 of the 256-row tiles an XCD may have two rounds left where others
   // have none: FP8 ragged 638 -> 609 us, weight gradients 2-10%) and fewer
@@ -407,7 +409,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
           c.part = n - at * parts;
         }
       }
-      c.g = __builtin_amdgcn_readfirstlane(s_pre[at]);
+      c.g = EIGHT != kNone8 ? __builtin_amdgcn_readfirstlane(s_pre[at]) : at;
       local = t - n * p.tiles_m * p.tiles_n;
       mtiles = p.tiles_m;
     } else {
