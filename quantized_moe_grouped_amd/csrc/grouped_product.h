@@ -102,13 +102,13 @@ struct Params {
   int32_t e, cumulative;     // groupList holds ends (type 0) instead of counts
   int32_t tiles_m, tiles_n;  // tiles along M (wgrad) and N
   int32_t out, accumulate;
+  int32_t grid;              // workgroups (gridDim lies behind all this, a line of arguments more to fetch: 0.25 us)
   // gated forms: what is kept of both projections (an output, or the way back's
   // input) as (m, 2 n') with n' the columns of h, and h itself (way back)
   void* kept;
   uint8_t* kept_scale;       // E8M0 (m, 2 n'/32) where it is kept in FP8
   void* hidden;
   int32_t keep, act;
-  int32_t grid;              // workgroups (gridDim lies behind all this, a line of arguments more to fetch: 0.25 us)
   int32_t splits;            // weight gradient of FP8 rows: parts of every group's rows
 };
 
@@ -372,6 +372,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   group_table(p, WGRAD ? 1 : BM, s_ends, s_pre);
   const int parts = EIGHT != kNone8 ? p.splits : 1;
   const int total = WGRAD ? p.e * parts * p.tiles_m * p.tiles_n : s_pre[p.e];
+  if constexpr (EIGHT != kNone8) length_order(p, s_ends, s_pre);  // the tiles' numbers need no table here
   const int64_t F = GLU ? p.n / 2 : p.n;  // columns of y
   const int64_t x_row = WGRAD ? p.k * (X8 ? 1 : 2) : p.k * XBITS / 8;  // bytes
   const int64_t w_row = WCOL ? p.n * (W8 ? 1 : 2) : p.k * WBITS / 8;
@@ -379,7 +380,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   const bool s_split = MX && (s_row & 3) != 0;  // k % 128 == 64: odd rows' scales begin mid-dword
 
   // ---- tiles: blocks of neighbouring raster tiles are dealt to the XCDs
-  if constexpr (EIGHT != kNone8) length_order(p, s_ends, s_pre);  // the tiles' numbers need no table here
   // (workgroup b runs on XCD b % 8), as many a block as its 32 CUs run at once
   // (with 64 of the 256-row tiles an XCD may have two rounds left where others
   // have none: FP8 ragged 638 -> 609 us, weight gradients 2-10%) and fewer
@@ -1641,6 +1641,7 @@ hipError_t launch(Plan& pl, hipStream_t s) {
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
   constexpr int STS = ENC == kFp8 ? 3 : (ENC == kFp4 ? 4 : 5);
   constexpr bool FOUR = WGRAD || FORM == kBackFull || FORM == kBackFp8;  // waves of 128 x 128
+  pl.p.grid = pl.grid;
   void* args[] = {&pl.p};
   if (pl.kind == kLarge)
     // The weight gradient's stages are whole rows of a tile whatever their
@@ -1667,4 +1668,3 @@ hipError_t launch(Plan& pl, hipStream_t s) {
 }
 
 }  // namespace gmmgm
-  pl.p.grid = pl.grid;
