@@ -31,7 +31,10 @@ int wgrad_run(const gmmgw_args* a, void* stream) {
   const int st = wgrad_plan(a, &pl);
   if (st != GMMFR_OK) return st;
   hipStream_t s = (hipStream_t)stream;
-  const hipError_t done = pl.enc == kBf16 ? launch<kBf16, true, true, true, false>(pl, s) : launch<kF16, true, true, true, false>(pl, s);
+  const hipError_t done = pl.enc == kBf16 ? (pl.few ? launch<kBf16, true, true, true, false, kStore, true>(pl, s)
+                                                    : launch<kBf16, true, true, true, false>(pl, s))
+                                          : (pl.few ? launch<kF16, true, true, true, false, kStore, true>(pl, s)
+                                                    : launch<kF16, true, true, true, false>(pl, s));
   return done == hipSuccess ? GMMFR_OK : GMMFR_ERR_HIP;
 }
 

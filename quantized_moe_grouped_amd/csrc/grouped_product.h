@@ -32,9 +32,16 @@
 //     then holds four neighbouring columns of one row, and a swap of two
 //     registers between the wave's halves makes them eight, stored in 16
 //     bytes.
-//   - Fragments of the next slice are read between the present one's products
-//     (one after the other before them they hold the LDS, and the waves' issue:
-//     weight gradient 1133 -> 1097 us, the gated block 1815 -> 1787).
+//   - Fragments of the next slice are read between the present one's products in
+//     the 256-row tiles: all at once before them they hold the LDS, and the
+//     waves' issue (bf16 and FP4 products 1-2% slower, the gated forms 1-2%,
+//     weight gradients of 1024 rows an expert and more 4%, those of FP8 rows
+//     2-4%).  Before them (EARLY) where that costs nothing and the reads
+//     between them do: 128-row tiles, whose two workgroups a CU hide each
+//     other's (between: 1-2% slower; not those of FP8 rows, alike), FP8 with FP4
+//     (2-4%), and 16-bit weight gradients of shorter groups (16 experts of 1024 x
+//     1024, 200 rows each that are not in the caches: 25 us, between 26 to 30 from
+//     box to box).
 //
 // What bounds it (one MI355X; rows over experts):
 //   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.90 to 0.95
@@ -295,9 +302,10 @@ __device__ __forceinline__ void one_of(int i, F&& f) {
 // epilogue; the tile's columns alternate 32 gate columns and the 32 up columns
 // that belong to them.  KWAVES: all waves compute the whole tile, each on its
 // own slice of every stage, and their sums meet in LDS (few rows: the weights
-// are streamed once and the tile is narrow).
+// are streamed once and the tile is narrow).  EARLY: a slice's fragments are
+// read before the products of the one before it, not between them.
 template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int BM, int BN, int BK, int WM, int WN, int STAGES,
-          bool KWAVES, int OCC, int FORM = kStore, int EIGHT = kNone8>
+          bool KWAVES, int OCC, int FORM = kStore, int EIGHT = kNone8, bool EARLY = (BM < 256 && EIGHT == kNone8) || ENC == kFp8>
 __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
   constexpr int NWAVES = WM * WN, NT = NWAVES * 64;
   constexpr bool MX = ENC == kFp4 || ENC == kFp8;
@@ -1297,13 +1305,14 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
       };
       auto with_copies = [&](XFrag (&x)[FM], WFrag (&w)[FN], auto s_, auto part_, int to, auto t_) {
         constexpr int T = decltype(t_)::value;  // the slice whose fragments are read meanwhile, of stage `to`
-        if constexpr (ALIVE)
+        if constexpr (ALIVE) {
+          if constexpr (EARLY) read_frags(to, T, xf[T & 1], wf[T & 1]);
           multiply(x, w, s_, [&](auto m_) {
-            read_after(to, T, xf[T & 1], wf[T & 1], m_);
+            if constexpr (!EARLY) read_after(to, T, xf[T & 1], wf[T & 1], m_);
             copies(refill, part_, m_);
             widened(part_, m_);
           });
-        else static_for<PRODUCTS>([&](auto m_) { copies(refill, part_, m_); });
+        } else static_for<PRODUCTS>([&](auto m_) { copies(refill, part_, m_); });
       };
 #pragma unroll 1
       for (int kt = 0; kt < steps; ++kt) {
@@ -1321,7 +1330,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
             with_copies(xf[0], wf[0], s_, Second{}, st, std::integral_constant<int, S + 1>{});
             advance();
           } else if constexpr (ALIVE) {
-            multiply(xf[S & 1], wf[S & 1], s_, [&](auto m_) { read_after(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1], m_); });
+            if constexpr (EARLY) read_frags(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1]);
+            multiply(xf[S & 1], wf[S & 1], s_, [&](auto m_) {
+              if constexpr (!EARLY) read_after(st, S + 1, xf[(S + 1) & 1], wf[(S + 1) & 1], m_);
+            });
           }
         });
         publish(kt + 1 < steps ? kt + 1 : 0);
@@ -1404,6 +1416,7 @@ struct Plan {
   Kind kind;
   int enc, grid;
   bool glu, col;
+  bool few;  // weight gradient: its groups are short
 };
 
 // tuning: [0] expected rows per expert, [1] forced tile height, [2] cap of the grid
@@ -1617,6 +1630,7 @@ inline int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   pl->kind = height ? (height == 256 ? kLarge : kMiddle)
              : few  ? kMiddle
                     : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n, false);
+  pl->few = m < 1024 * e;  // (fragments read early: see above; 375 rows 28.9 us, between 29 to 33; 1024: 45.7, 44.4)
   p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);
   p.tiles_n = (int32_t)ceil_div(n, kTileN[pl->kind]);
   pl->grid = grid_of(*pl, e * p.tiles_m * p.tiles_n, cap);
@@ -1635,7 +1649,7 @@ inline int describe(int status, const Plan& pl, gmmgm_plan_info* info) {
 
 // (hipLaunchKernel gives this launch's own status, where the runtime's last
 // error may be an earlier one of the program's)
-template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int FORM = kStore>
+template <int ENC, bool XCOL, bool WCOL, bool WGRAD, bool GLU, int FORM = kStore, bool EARLY = ENC == kFp8>
 hipError_t launch(Plan& pl, hipStream_t s) {
   const size_t dyn = (size_t)(2 * pl.p.e + 1) * 4;
   constexpr int BK = ENC == kFp4 ? 256 : (ENC == kFp8 ? 128 : 64), BKS = ENC == kFp8 ? 256 : BK;
@@ -1651,7 +1665,7 @@ hipError_t launch(Plan& pl, hipStream_t s) {
     // of 128 x 128 read a third less from LDS than eight of 64 x 128, which
     // transposing reads make up for (1.20 -> 1.12 ms; without them -1 .. +2%).
     return hipLaunchKernel((const void*)product_kernel<ENC, XCOL, WCOL, WGRAD, GLU, 256, 256, WGRAD ? BK / 2 : BK,
-                                                       FOUR ? 2 : 4, 2, WGRAD ? 4 : 2, false, FOUR ? 1 : 2, FORM>,
+                                                       FOUR ? 2 : 4, 2, WGRAD ? 4 : 2, false, FOUR ? 1 : 2, FORM, kNone8, EARLY>,
                            dim3(pl.grid), dim3(FOUR ? 256 : 512), args, dyn, s);
   if constexpr (!WGRAD) {
     if constexpr ((ENC == kBf16 || ENC == kF16) && !WCOL && (!GLU || FORM == kGated)) {
