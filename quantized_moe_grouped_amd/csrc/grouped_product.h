@@ -1588,7 +1588,8 @@ inline int product_plan(const gmmgm_args* a, Plan* pl, int more = 0) {
   return GMMFR_OK;
 }
 
-inline int wgrad_plan(const gmmgw_args* a, Plan* pl) {
+// eight: one of the two is kept in FP8.
+inline int wgrad_plan(const gmmgw_args* a, Plan* pl, bool eight = false) {
   if (!a) return GMMFR_ERR_NULLPTR;
   if (!given(a->x) || !given(a->dy) || !given(a->group_list) || !given(a->dw)) return GMMFR_ERR_NULLPTR;
   const int xt = a->x.dtype, ot = a->dw.dtype;
@@ -1623,12 +1624,28 @@ inline int wgrad_plan(const gmmgw_args* a, Plan* pl) {
   pl->glu = false;
   pl->col = true;
   // Few rows an expert are a few steps: with results of 16 bits, which do not
-  // fill the memory's time, two workgroups a CU hide the tiles' ends (us under
-  // 128-row and 256-row tiles, 32 experts of 2048 x 2048, bf16 results: 8 rows
-  // 71, 85, 64 rows 94, 94, 128 rows 115, 111; fp32: 8 rows 148, 110).
-  const bool few = ot != GMMFR_DT_FLOAT32 && m <= 64 * e;
+  // fill the memory's time, two workgroups a CU hide the tiles' ends, but read
+  // each row twice as often.  So the 128-row tiles are taken where the others
+  // make two rounds of the chip at most, or a sixteenth more work at the ends of
+  // rounds and matrices, or where the rows are fewest beside the columns (us
+  // under 128-row and 256-row tiles, rows and results not in the caches):
+  //   two rounds      4 of 2048 x 2048, 8 rows   15.3, 17.8   64 of 512 x 512, 64 rows    16.5, 18.7
+  //   less work       4 of 7168 x 2048, 64 rows  40, 48       64 of 2880 x 2880, 64 rows  343, 379
+  //   fewest rows     16 of 4096 x 8192, 8 rows  293, 330     64 of 2048 x 2048, 4 rows   165, 171
+  //   none of them    64 of 2048 x 2048, 64 rows 188, 179     64 of 1024 x 4096, 64 rows  204, 174
+  //                   16 of 2048 x 4096, 16 rows 94, 88       64 of 1024 x 1024, 64 rows  52.6, 48.5
+  // (results in fp32, in the caches: 32 of 2048 x 2048, 8 rows 148, 110).  Rows
+  // kept in FP8 cost half of that, and something a step of 32 of them: the
+  // 128-row tiles for one step (64 of 1536 x 2048: 4 rows 129, 145, 32 rows 135,
+  // 145, 48 rows 146, 145, 64 rows 152, 143; 64 of 1024 x 4096: 32 rows 190,
+  // 183, 48 rows 206, 183).
+  const int64_t large = e * ceil_div(k, 256) * ceil_div(n, 256), middle = e * ceil_div(k, 128) * ceil_div(n, 128);
+  const int64_t rounds = ceil_div(large, 256);
+  const bool fine = ot != GMMFR_DT_FLOAT32 &&
+                    (eight ? m <= 32 * e
+                           : m <= 64 * e && (rounds <= 2 || middle * 8 <= 15 * 512 * rounds || (k >= 2048 && 512 * m <= e * k)));
   pl->kind = height ? (height == 256 ? kLarge : kMiddle)
-             : few  ? kMiddle
+             : fine ? kMiddle
                     : larger_kind(2 * e * ceil_div(k, 256), 2 * e * ceil_div(k, 128), n, false);
   pl->few = m < 1024 * e;  // (fragments read early: see above; 375 rows 28.9 us, between 29 to 33; 1024: 45.7, 44.4)
   p.tiles_m = (int32_t)ceil_div(k, kTileM[pl->kind]);

@@ -82,7 +82,7 @@ int wgrad_fp8_plan(const gmmgx_args* a, Plan* pl, bool* x8, size_t* workspace) {
   wide.accumulate = a->accumulate;
   wide.tuning_config = a->tuning_config;
   wide.tuning_config_len = a->tuning_config_len;
-  const int st = wgrad_plan(&wide, pl);
+  const int st = wgrad_plan(&wide, pl, true);
   if (st != GMMFR_OK) return st;
   const int64_t columns = *x8 ? pl->p.k : pl->p.n;
   if (columns % 64 != 0 || !shape_is(scale, 3, pl->p.m, columns / 64, 2)) return GMMFR_ERR_SHAPE;
