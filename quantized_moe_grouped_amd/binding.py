@@ -680,14 +680,15 @@ def _grouped_matmul_wgrad(handle, x, dy, group_list, x_scale, dy_scale, out, out
         _enqueue("gmm_grouped_matmul_wgrad", raw, workspace, handle)
     else:
         raw = _gx_bytes(x, dy, x_scale, dy_scale, group_list, out, group_list_type, accumulate, tail)
-        if workspace is None and x.shape[0] >= 2048 * group_list.shape[0]:  # else none is wanted
-            need = ctypes.c_size_t(0)
-            st = lib().gmm_grouped_matmul_wgrad_fp8_workspace(raw, ctypes.byref(need))
-            if st != OK:
-                raise GmmfrError(st, "gmm_grouped_matmul_wgrad_fp8")
-            if need.value:
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        _enqueue("gmm_grouped_matmul_wgrad_fp8", raw, workspace, handle)
+        try:
+            _enqueue("gmm_grouped_matmul_wgrad_fp8", raw, workspace, handle)
+        except GmmfrError as e:
+            if workspace is not None or e.code != ERR_WORKSPACE:
+                raise
+            need = ctypes.c_size_t(0)  # one is wanted: nothing was launched without it
+            lib().gmm_grouped_matmul_wgrad_fp8_workspace(raw, ctypes.byref(need))
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+            _enqueue("gmm_grouped_matmul_wgrad_fp8", raw, workspace, handle)
     del tuning
     return out
 
