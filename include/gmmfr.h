@@ -420,8 +420,9 @@ int gmm_grouped_matmul_wgrad(const gmmgw_args* args, void* workspace, size_t wor
 /*
  * The same where one of the two was kept in FP8: the rows that the forward pass
  * multiplied (gmm_mx_quantize), as x, or as dy for weights kept as (e,n,k).  A
- * value is its code times its block's scale, brought to the other operand's
- * type (exact in BFLOAT16, rounded to nearest in FLOAT16); the result is that
+ * value is its code times its block's scale, brought to the nearest of the other
+ * operand's type (BFLOAT16: the value itself under scales of 2^-124 and more;
+ * FLOAT16: infinite past 65504, with fewer bits below 2^-14); the result is that
  * of gmm_grouped_matmul_wgrad on such values, to the bit, unless the plan splits
  * the groups' rows (few tiles, 2048 rows an expert and more): then the parts'
  * fp32 sums meet in the workspace, in one order whatever the launch.

@@ -658,8 +658,10 @@ def grouped_matmul_wgrad(x, dy, group_list, *, x_scale=None, dy_scale=None, out=
     accumulate: added to `out` (fp32).  Weights kept as (e,n,k): pass (dy, x).
     One of the two may be in FP8 with its scales (x_scale or dy_scale, as
     mx_quantize makes them): the result is that of the same values in the other
-    operand's type, but for the order of additions where the rows of few, long
-    groups are split (a workspace is allocated then, if none is given).  With a gate dy is the gradient of the product before it
+    operand's type (beside an fp16 operand those past 65504 are infinite, and
+    those below 2^-14 lose bits), but for the order of additions where the rows
+    of few, long groups are split (a workspace is allocated then, if none is
+    given).  With a gate dy is the gradient of the product before it
     (gated_matmul_backward)."""
     dev = _check_tensors(x, dy, group_list, x_scale, dy_scale, out, workspace)
     if accumulate and out is None:

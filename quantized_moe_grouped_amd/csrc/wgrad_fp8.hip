@@ -6,11 +6,12 @@
 // Scales lie across the reduction, which the scaled matrix instructions cannot
 // take (theirs lie along it), so codes become 16-bit values on their way: they
 // are copied to LDS as they are, half the bytes, and the thread that copied
-// sixteen of a row turns them into 16-bit values (one instruction for two, exact
-// in bf16), a step before the matrix core has them.  In fp16, values past
-// 65504 become infinite and those below 2^-14 lose bits.  The sums are those of
-// the 16-bit weight gradient on the widened rows, to the bit, where the groups'
-// rows are not split.
+// sixteen of a row turns them into 16-bit values (one instruction for two), a
+// step before the matrix core has them: the nearest of the type.  bf16 holds all
+// of them under scales of 2^-124 and more, and below that those from its least
+// subnormal, 2^-133, on; in fp16 values past 65504 become infinite and those
+// below 2^-14 lose bits.  The sums are those of the 16-bit weight gradient on the
+// widened rows, to the bit, where the groups' rows are not split.
 //
 // 32768 rows over 32 experts, 7168 x 4096, fp32 results (one MI355X): 2.26 to
 // 2.32 ms, 0.83 to 0.85 PFLOP/s, the 16-bit gradient of the same rows 2.24,
