@@ -246,10 +246,11 @@ static __device__ void group_table(const Params& p, int bm, int32_t* s_ends, int
 // The experts whose groups are longer than twice the average first, the others
 // from the end: a weight gradient's tiles last as long as their group, and long
 // ones that began last would run alone (FP8 rows, 6007 of them skewed over 48 of
-// 1088 x 1600, results of 16 bits: 121 -> 105 us).  Not for rows of 16 bits: over
-// thirty skewed lists it took between 10% less and 13% more, and 2% more of even
-// ones.  One round of 64 experts a time, few instructions: every workgroup does
-// this before its first copy.
+// 1088 x 1600, results of 16 bits: 121 -> 105 us; over such lists of other sizes
+// between 15% less and 8% more).  Not for rows of 16 bits: over thirty skewed
+// lists it took between 10% less and 13% more, and 2% more of even ones.  One
+// round of 64 experts a time, few instructions: every workgroup does this before
+// its first copy.
 static __device__ void length_order(const Params& p, const int32_t* s_ends, int32_t* s_order) {
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
@@ -1065,9 +1066,6 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void product_kernel(Params p) {
     // last of them may need
     if constexpr (IN_AGPRS) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     if constexpr (BACK) {
-      // What was kept is asked for AHEAD blocks before it is used: loads and
-      // stores are counted together and in order, so that a load behind stores
-      // is waited for with them.
       // One loop over the blocks, whose sums are brought to the same registers:
       // unrolled it would be 30 KB of instructions that every wave fetches once
       // a tile.  What was kept is asked for three blocks ahead: loads and stores
@@ -1559,8 +1557,10 @@ inline int product_plan(const gmmgm_args* a, Plan* pl, int more = 0) {
                       (avg <= 16 ? !pl->col || middle <= 256
                                  : avg <= 32 && (pl->enc == kFp8 || middle <= (pl->col ? 128 : 256)));
   // One expert's rows are known but for those behind it: whole tiles of them
-  // (4096 rows of 7168 bf16 (e,n,k), us under 128-row and 256-row tiles: n =
-  // 4096 with a gate 218, 183, n = 2048 112, 135).
+  // (4096 rows of 7168, us under 128-row and 256-row tiles; inputs not in the
+  // caches, and in them):
+  //   n = 4096   bf16 (e,n,k) 249, 205 and 216, 183   FP4 95, 76 and 89, 72   FP8 147, 118 and 124, 99
+  //   n = 2048   bf16 (e,n,k) 148, 198 and 113, 146   FP4 54, 74 and 53, 65   FP8 81, 110 and 71, 92
   auto along = [&](int64_t t) {
     if (parts == 1) return 2 * ceil_div(rows > 0 ? rows : m, t);
     if (rows > 0) return 2 * busy * ceil_div(rows, t);
@@ -1582,6 +1582,7 @@ inline int product_plan(const gmmgm_args* a, Plan* pl, int more = 0) {
   // microscaled ones are staged for 64 columns.  us, 64 columns against 32:
   //   7168 x 4096, 1 row    64 tiles  34, 24    16384 x 8192      128  74, 59
   //   8 of 2048 x 1024     128        14, 11    16 of 2048 x 1024 256  18, 18
+  // (in the caches; not in them the first 40, 27 and 77, 63 with a launch's events)
   if (pl->kind == kSmall && !mx && (!glu || (more & kThinGate)) && !pl->col && tiles <= 256) tiles = tiles_of(pl->kind = kThin);
   if (tiles >= (int64_t(1) << 31)) return GMMFR_ERR_SHAPE;
   pl->grid = grid_of(*pl, tiles, cap);

@@ -25,9 +25,11 @@ namespace gmmgm {
 
 // Where the tiles leave workgroups without one and groups are long, the rows of
 // each are split into parts of 1024 and more: their sums go to a workspace, one
-// after the other in memory, and sum_parts adds them in their order.  256-row
-// tiles if their parts fill three quarters of the chip (us, whole, and split with
-// 128-row and 256-row tiles; fp32 results):
+// after the other in memory, and sum_parts adds them in their order.  Long by the
+// average, as the host knows no more: a list with one long group among short ones
+// is not split, nor are 8000 rows over 4 experts of 512 x 512 (35 us, where 8192
+// rows take 27).  256-row tiles if their parts fill three quarters of the chip
+// (us, whole, and split with 128-row and 256-row tiles; fp32 results):
 //   1 of 1024 x 1024, 16384 rows  248,  59,  55    1 of 512 x 512, 8192 rows  124, 30, 46
 //   2 of 832 x 864, 25694         198,  69,  66    4 of 512 x 512, 16384       65, 31, 47
 //   1 of 2048 x 2048, 16384       240, 179, 140    1 of 128 x 128, 4096        64, 25, 39
