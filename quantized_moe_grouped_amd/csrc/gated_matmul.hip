@@ -13,10 +13,11 @@
 // What bounds it (one MI355X, bf16, inputs not in the caches):
 //   - forward, 32768 rows over 32 experts of 7168 x 2 2048, (e,k,n): 1.67 ms with
 //     nothing kept, 1.74 in 16 bits, 1.72 in FP8 = 1.12 PFLOP/s: the products
-//     (SwiGLU alone 1.70), matrix cores 68% busy at the clock that the card's
+//     (SwiGLU alone 1.70), matrix cores 67% busy at the clock that the card's
 //     power leaves; 12% more rows are multiplied than there are.
-//   - backward of the same from FP8: 1.04 ms.  The product alone takes 0.91; 0.41
-//     GB more are written and read a call, which is 0.08 ms at the copy rate.
+//   - backward of the same from FP8: 1.04 ms.  The product alone takes 0.91, half
+//     a round of 4.5 with half of the chip; 0.41 GB more are written and read a
+//     call, which is 0.08 ms at the copy rate.
 //     Timed in copies of the kernel: without the stores 0.99, without the loads
 //     1.05, without the gate's arithmetic 1.07 (of 1.09).
 //   - one token through 8 of 32 experts: the weights, 6.5 TB/s.

@@ -45,16 +45,16 @@
 //
 // What bounds it (one MI355X; rows over experts):
 //   - 16 bit, 256-row tiles, 32768 x 2048 x 7168 over 32, (e,k,n): 0.90 to 0.95
-//     ms from box to box, 1.02 to 1.06 PFLOP/s.  Matrix cores busy 64% of the
-//     cycles at the 1.74 GHz that the card's power leaves; between them the
-//     waits for LDS and barriers.
-//   - weight gradient of the same: 1.10 ms, 45% busy at 1.92 GHz: one
-//     workgroup a CU (its sums fill the registers), whose 1.9 GB of fp32
-//     results go out ahead of copies that the next tile's first step waits for.
+//     ms from box to box, 1.02 to 1.06 PFLOP/s.  Matrix cores busy 67% of the
+//     cycles at the clock that the card's power leaves (1.85 GHz, within three
+//     calls 1.31); between them the waits for LDS and barriers.
+//   - weight gradient of the same: 1.10 ms, 49% busy: one workgroup a CU (its
+//     sums fill the registers), whose 1.9 GB of fp32 results go out ahead of
+//     copies that the next tile's first step waits for.
 //   - FP4, 131072 x 7168 x 4096 over 32, SwiGLU: 2.01 to 2.08 ms, 3.7 to 3.8
-//     PFLOP/s, 51% busy at 1.76 GHz: a product is a quarter of the 16-bit one's
-//     time for the same bytes copied and read.
-//   - FP8 with FP4, 30001 x 2112 x 7152 over 64: 0.61 ms, 46% busy; a third of
+//     PFLOP/s, 54% busy: a product is a quarter of the 16-bit one's time for the
+//     same bytes copied and read.
+//   - FP8 with FP4, 30001 x 2112 x 7152 over 64: 0.61 ms, 47% busy; a third of
 //     the rows multiplied do not exist, and reads of 64-byte rows of weights
 //     conflict in 28% of the LDS' active cycles.
 //   - rows whose bytes are no multiple of 128 cost twice the requests to the

@@ -14,9 +14,9 @@
 // widened rows, to the bit, where the groups' rows are not split.
 //
 // 32768 rows over 32 experts, 7168 x 4096, fp32 results (one MI355X): 2.26 to
-// 2.32 ms, 0.83 to 0.85 PFLOP/s, the 16-bit gradient of the same rows 2.24,
-// widening them first 2.37 and a copy of them in memory.  Matrix cores 39% busy
-// at 1.92 GHz.  Timed in copies of the kernel: without its 3.8 GB of stores 1.88
+// 2.33 ms, 0.83 to 0.85 PFLOP/s, the 16-bit gradient of the same rows 2.24,
+// widening them first 2.37 and a copy of them in memory.  Matrix cores 40% busy
+// at 1.85 GHz.  Timed in copies of the kernel: without its 3.8 GB of stores 1.88
 // ms, of that without the copies 1.46, without reading fragments 1.69, without
 // widening 1.66.
 #include "grouped_product.h"
